@@ -247,6 +247,57 @@ MOE_API int moe_forward_mxfp8(moe_handle *h, const void *x, int32_t T, const voi
                               const float *router_bias, const moe_mxfp8_experts *w, int32_t top_k,
                               void *out, void *stream);
 
+/* ---- the gated feed-forward block, forward and backward -------------------------------------
+ * The layer equation's W_shared(x) term on its own, for any token count and any sizes: a dense
+ * layer's FFN, or the shared expert's training step.
+ *     u = x W_up^T,  g = x W_gate^T,  h = SiLU(u) (.) g,  out = h W_down^T
+ * (SiLU on the up projection, as in moe_forward.) With dout = dL/dout and s = 1 / (1 + exp(-u)):
+ *     dh = dout W_down,  dg = dh (.) u s,  du = dh (.) g (.) s (1 + u (1 - s)),
+ *     dx = du W_up + dg W_gate,  dW_up = du^T x,  dW_gate = dg^T x,  dW_down = dout^T h.
+ * Any handle of the device works: sizes are arguments, the handle only lends its device, its
+ * timeout and its status word, and all scratch memory is the caller's `workspace`. So calls on
+ * different streams may overlap if each has a workspace of its own, and a call may be captured in
+ * a CUDA graph as it is (the workspace then belongs to the graph). The device that was current
+ * stays current. Products are summed in fp32 in a fixed order: equal inputs give equal bits.
+ *   T       tokens, 0..2^24;  hidden H and inter D: multiples of 8, 8..2^20
+ *   w       device bf16: up [D][H], gate [D][H], down [H][D]
+ * Buffers must not overlap one another. MOE_ERR_INVALID_ARG for a null pointer, a bad size or a
+ * workspace that is too small, MOE_ERR_UNSUPPORTED for sizes beyond those above (and on a device
+ * without room for a pair of SMs), MOE_ERR_MISALIGNED for a pointer off a 16-byte boundary. */
+
+/* Workspace bytes of moe_ffn_forward (backward = 0) or moe_ffn_backward (1); -1 for sizes that
+ * they refuse. */
+MOE_API int64_t moe_ffn_workspace_bytes(int64_t T, int32_t hidden, int32_t inter, int32_t backward);
+
+/*   x         device bf16 [T][H] (may be NULL when T == 0, as may out and workspace)
+ *   out       device [T][H], bf16 (out_bf16 = 1, rounded once) or fp32 (0); fully overwritten
+ *   u, g      device bf16 [T][D], both or neither: the pre-activations that moe_ffn_backward
+ *             needs, rounded once (h is computed from the unrounded sums)
+ * h is rounded to bf16 before the down projection, as in moe_forward. */
+MOE_API int moe_ffn_forward(moe_handle *h, const void *x, int64_t T, int32_t hidden, int32_t inter,
+                            const moe_shared_w *w, void *out, int32_t out_bf16, void *u, void *g,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Weight gradients, shaped as the weights: bf16, or fp32 with MOE_FFN_GRAD_F32. Each may be NULL:
+ * it is then not computed. */
+typedef struct moe_ffn_grads {
+    void *up;
+    void *gate;
+    void *down;
+} moe_ffn_grads;
+#define MOE_FFN_GRAD_F32 1u  /* the weight gradients are fp32 buffers */
+#define MOE_FFN_GRAD_ADD 2u  /* add to what they hold (needs MOE_FFN_GRAD_F32) instead of overwriting */
+
+/*   dout      device bf16 [T][H];  x, u, g: the forward's input and pre-activations
+ *   dx        device bf16 [T][H], or NULL: not computed
+ *   grads     nullable; see above
+ * du, dg and h are rounded to bf16 before the products that read them (the tensor cores' operand
+ * type). With T == 0 the weight gradients are zeroed (or, with MOE_FFN_GRAD_ADD, left alone). */
+MOE_API int moe_ffn_backward(moe_handle *h, const void *dout, const void *x, const void *u,
+                             const void *g, int64_t T, int32_t hidden, int32_t inter,
+                             const moe_shared_w *w, void *dx, const moe_ffn_grads *grads,
+                             uint32_t flags, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Makes `stream` wait for every copy back queued by moe_forward_host_async on this handle; with
  * `block` non-zero the host also waits for them. */
 MOE_API int moe_forward_host_join(moe_handle *h, void *stream, int32_t block);
@@ -254,7 +305,8 @@ MOE_API int moe_forward_host_join(moe_handle *h, void *stream, int32_t block);
 /* Synchronise the handle's last stream and report the device status word:
  * *device_status = 0 when every kernel since the last call finished normally, else a
  * device error code (bit 30 set, low bits naming the wait that ran out). The word is
- * cleared by this call. Returns MOE_ERR_DEVICE_TIMEOUT if a wait ran out, MOE_ERR_CUDA if
+ * cleared by this call. It also covers the moe_ffn_* calls: after one of their waits ran out, the
+ * handle's later ones give up at once, until this call has reported it. Returns MOE_ERR_DEVICE_TIMEOUT if a wait ran out, MOE_ERR_CUDA if
  * the stream reported a CUDA error, else MOE_OK. */
 MOE_API int moe_get_status(moe_handle *h, int32_t *device_status);
 
@@ -332,7 +384,8 @@ MOE_API int moe_stage_times(moe_handle *h, float *ms, int32_t n);
  * 4 MXFP8, 5 two-tile), 9 rows of the per-row buffers of moe_debug_expert_rows, 10 their h row stride
  * (elements, max(D, D_shared)), 11 kernels the last forward launched (1 for a fused small
  * batch, else 6), 12 whether batches of at most 16 tokens run fused on this handle (1) or not
- * (for moe_forward_mxfp8 on a handle made with MOE_FLAG_MXFP8, else for moe_forward). */
+ * (for moe_forward_mxfp8 on a handle made with MOE_FLAG_MXFP8, else for moe_forward), 13 the
+ * handle's device ordinal. */
 MOE_API int moe_query(const moe_handle *h, int32_t which, int64_t *value);
 
 /* Per-task trace of the last forward (needs MOE_FLAG_TRACE; synchronises). Fills up to

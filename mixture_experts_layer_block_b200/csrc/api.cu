@@ -10,113 +10,23 @@
 #include <new>
 #include <vector>
 
-#include "launch.h"
-#include "moe_b200.h"
-#include "mx.cuh"
+#include "handle.h"
 
 namespace moe {
 cudaError_t configure_router_kernel();
 cudaError_t configure_gemm_kernel();
 cudaError_t configure_gemm_pair_kernel(int* max_pairs);
 int small_fused_blocks_per_sm();
+cudaError_t configure_ffn_kernels(int* max_pairs);
 }  // namespace moe
 
 using namespace moe;
 
 namespace {
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-struct MapKey {
-  const void* ptr;
-  uint64_t inner, outer, stride;
-  uint32_t box0, box1;
-  int dtype;
-  bool operator==(const MapKey& o) const {
-    return ptr == o.ptr && inner == o.inner && outer == o.outer && stride == o.stride &&
-           box0 == o.box0 && box1 == o.box1 && dtype == o.dtype;
-  }
-};
-
-struct MapEntry {
-  MapKey key;
-  CUtensorMap map;
-};
-
-constexpr int64_t kDefaultTimeoutNs = 2000000000LL;
 constexpr size_t kMapCacheMax = 64;
 constexpr int kTimingRing = 256;  // forwards whose kernel durations moe_stage_times averages
 constexpr int kNumStages = 6;     // router, gating, align scatter, row gather, expert GEMMs, combine
-
-}  // namespace
-
-struct moe_handle {
-  moe_config cfg{};
-  int device = 0;
-  int num_sms = 0;
-  char* ws_mem = nullptr;
-  size_t ws_bytes = 0;
-  Workspace ws{};
-  int max_tiles = 0, max_lag = 0, max_units = 0;
-  int64_t sorted_len_max = 0, blocks_len_max = 0;
-  size_t gate_smem = 0;
-  EncodeTiledFn encode = nullptr;
-  std::vector<MapEntry> cache;
-  CUtensorMap h_routed{}, h_shared{}, xs_map{}, y_map{};
-  CUtensorMap h_routed16{}, h_shared16{}, xs_map16{};  // 16-row boxes for batches of <= 16 tokens
-  CUtensorMap h_routed32{}, h_shared32{}, xs_map32{}, y_map32{};  // 32-row boxes (SM-pair tiles)
-  int max_routed_tiles = 0;
-  int64_t routed_rows = 0, tile_rows = 0;  // rows of xs, and of h and y, for either tile height
-  int max_pairs = 0;                       // 2-CTA clusters of the pair kernel that fit at once
-  int last_workers = 0, last_tile_m = kBM;
-  int last_shape = 0;  // expert-GEMM shape of the last forward: 0 general, 1 small, 2 tail, 3 pair
-  int last_kernels = 0;  // kernels launched by the last forward
-  bool fused_ok = false;  // batches of <= 16 tokens may run as one fused launch on this device
-  bool mx_fused_ok = false;  // the same for moe_forward_mxfp8
-  int32_t epoch = 0;      // fused forwards launched (the arrival counter's target / grid size)
-  int parts_rows = 0;  // rows of the K-split partial logits buffer
-  std::vector<cudaEvent_t> ev;  // kTimingRing x (kNumStages + 1) events around the kernels
-  int timed = 0;                // forwards recorded since the last moe_stage_times
-  bool timing = false;
-  cudaStream_t last_stream = nullptr;
-  bool have_forward = false;
-  int last_T = 0, last_k = 0, last_lag = 0;
-  void* x_stage = nullptr;   // [2 slots][max_tokens][H] bf16 (slot 0 for moe_forward_host)
-  float* out_stage = nullptr;  // [2 slots][max_tokens][H] fp32 or bf16
-  size_t x_slot_bytes = 0, out_slot_bytes = 0;
-  // moe_forward_host_async: copy streams and, per staging slot, the events that order the
-  // copy in, the forward and the copy back
-  cudaStream_t copy_in = nullptr, copy_out = nullptr;
-  cudaEvent_t ev_in[2] = {nullptr, nullptr}, ev_done[2] = {nullptr, nullptr}, ev_out[2] = {nullptr, nullptr};
-  bool slot_used[2] = {false, false};
-  int async_slot = 0;
-  bool async_pending = false;
-  int dep_extra_next = 0;
-  int64_t timeout_ns = kDefaultTimeoutNs;
-  // MXFP8 workspace (MOE_FLAG_MXFP8): x in token order and in tile order, h, with their scales
-  MxBuffers mx{};
-  CUtensorMap mx_xs_map{}, mx_h_map{}, mx_xs_map32{}, mx_h_map32{};
-};
-
-namespace {
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int encode_map(moe_handle* h, CUtensorMap* out, const void* ptr, uint64_t inner, uint64_t outer,
-               uint64_t stride_bytes, uint32_t box0, uint32_t box1,
-               CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {stride_bytes};
-  cuuint32_t box[2] = {box0, box1};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = h->encode(out, dtype, 2, const_cast<void*>(ptr), dims,
-                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
-}
 
 // Weight maps are cached by (pointer, shape, box): encoding is cheap, but caching keeps the
 // per-call host work to a lookup.
@@ -176,8 +86,6 @@ Shape make_shape(const moe_handle* h, int T, int k, int tile_m = kBM, int worker
   return sh;
 }
 
-int check_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
 // Router N tile: the narrowest power of two >= E (at most kRouterMaxN, so that x is read once
 // per K split), narrowed while the m-tiles x N tiles x the deepest K split give less than half
 // a wave of CTAs (a few tokens then still spread the router weights over many SMs).
@@ -188,8 +96,6 @@ int router_bn(int E, int T, int num_sms) {
   while (bn > 16 && (int64_t)mt * ceil_div(E, bn) * kMaxRouterSplits < num_sms / 2) bn /= 2;
   return bn;
 }
-
-int select_device(moe_handle* h) { return check_cuda(cudaSetDevice(h->device)); }
 
 }  // namespace
 
@@ -288,6 +194,7 @@ int moe_init(const moe_config* cfg, moe_handle** out) {
   const size_t T_pad = (size_t)ceil_div(c.max_tokens, kBM) * kBM;
   std::vector<Piece> pieces = {
       {(void**)&w.meta, sizeof(DeviceMeta)},
+      {(void**)&h->ffn_meta, sizeof(DeviceMeta)},
       {(void**)&w.logits, T_ * E_ * 4},
       {(void**)&w.logit_parts, (size_t)h->parts_rows * E_ * 4},
       {(void**)&w.topk_ids, T_ * K_ * 4},
@@ -424,6 +331,8 @@ int moe_init(const moe_config* cfg, moe_handle** out) {
   h->mx_fused_ok = coop != 0 && E <= kFusedMaxExperts && (c.flags & MOE_FLAG_MXFP8) &&
                    mx_small_fused_blocks_per_sm() >= 1 && !(c.flags & MOE_FLAG_UNFUSED_SMALL);
   h->max_pairs = std::min(h->max_pairs, h->num_sms / 2);
+  if (check_cuda(configure_ffn_kernels(&h->ffn_pairs))) return fail(MOE_ERR_CUDA);
+  h->ffn_pairs = std::min(h->ffn_pairs, h->num_sms / 2);
   h->last_workers = h->num_sms;
   if (h->timing) {
     h->ev.assign((size_t)kTimingRing * (kNumStages + 1), nullptr);
@@ -894,6 +803,13 @@ int moe_get_status(moe_handle* h, int32_t* device_status) {
   const int32_t zero = 0;
   if (cudaMemcpy(&h->ws.meta->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
     return MOE_ERR_CUDA;
+  // the feed-forward block's own words: an abort there stays until it is reported here
+  DeviceMeta fm{};
+  if (cudaMemcpy(&fm, h->ffn_meta, sizeof fm, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
+  if (fm.status != 0 || fm.abort != 0) {
+    if (cudaMemset(h->ffn_meta, 0, sizeof fm) != cudaSuccess) return MOE_ERR_CUDA;
+    if (st == 0) st = fm.status;
+  }
   if (device_status) *device_status = st;
   if (st & kStatusTimeout) return MOE_ERR_DEVICE_TIMEOUT;
   return MOE_OK;
@@ -1032,6 +948,7 @@ int moe_query(const moe_handle* h, int32_t which, int64_t* value) {
     case 10: *value = h->ws.ldh; return MOE_OK;
     case 11: *value = h->last_kernels; return MOE_OK;
     case 12: *value = ((h->cfg.flags & MOE_FLAG_MXFP8) ? h->mx_fused_ok : h->fused_ok) ? 1 : 0; return MOE_OK;
+    case 13: *value = h->device; return MOE_OK;
     default: return MOE_ERR_INVALID_ARG;
   }
 }

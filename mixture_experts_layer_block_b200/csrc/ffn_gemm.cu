@@ -1,0 +1,569 @@
+// ffn_gemm.cu -- the matrix products of the gated feed-forward block and of its backward pass
+// (ffn.cuh gives the formulas) as one persistent GEMM on pairs of SMs.
+//
+// What bounds it: at training sizes the tensor cores; at a few hundred tokens the weights' bytes.
+// Each output tile of 256 x bn (bn <= 256) belongs to a cluster of two CTAs: one
+// tcgen05.mma.cta_group::2 (M = 256) per 16-wide K step, issued by CTA 0, with 128 rows of A and
+// bn / 2 rows of B staged by each CTA. A pair moves 32 KB per SM and 64-wide K step where a
+// 128 x 256 tile on one SM needs 48 KB for the same work. Two accumulators fill the tensor memory,
+// so that the epilogue of one tile runs under the products of the next.
+//
+// Operands come as they lie in memory. A K-major operand is one TMA box of {64 k, rows}; an
+// MN-major one (the weights of the backward products, and both operands of the weight gradients)
+// is boxes of {64 m or n, 64 k}, which the MMA reads through an MN-major descriptor: no transposed
+// copy is ever made. Everything past an edge is filled with zeros by TMA on both operands, and
+// clipped on the way out.
+//
+// The units (tile, K split) of up to four products form one list (the four gradients that depend
+// on du, dg and h run as one launch), dealt round robin to the pairs: with equal units per
+// product this is as even as a shared counter and needs no state in memory. With fewer tiles than pairs
+// K is split; the partial sums go to a workspace in fp32 and ffn_reduce_kernel adds them in split
+// order, so that results do not depend on timing.
+//
+// Warp roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (CTA 0), warps 2-5 epilogue.
+#include <algorithm>
+
+#include "ffn.cuh"
+#include "launch.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kFThreads = 192;
+constexpr int kFMaxStages = 8;
+constexpr int kFABytes = 128 * kBK * 2;  // 16 KB of A per CTA and stage
+constexpr int kFBoxBytes = 64 * 64 * 2;  // an MN-major box of 64 x 64
+constexpr int kFChunk = 32;              // columns per epilogue step
+constexpr int kFBarBytes = 256;
+constexpr int kFSmem = 227 * 1024 - 1024;  // less the alignment slack
+// three results per tile (h, u, g or du, dg, h) are staged at once, twice
+__host__ __device__ constexpr int staging_bytes(int epi) { return epi == kFfnStore ? 32 * 1024 : 48 * 1024; }
+__host__ __device__ constexpr int ring_bytes(int epi) { return kFSmem - staging_bytes(epi) - kFBarBytes; }
+
+// B's bytes per CTA and stage: bn / 2 rows of 128 bytes, or whole 64-wide boxes
+__host__ __device__ inline int b_bytes(int bn, int b_mn) {
+  return b_mn ? ((bn / 2 + 63) / 64) * kFBoxBytes : (bn / 2) * 128;
+}
+
+// Descriptor of an MN-major bf16 operand with the 128-byte swizzle: 64-element rows of 128 bytes
+// (m or n contiguous), 8 k to a 1024-byte atom, atoms along k 1024 bytes apart (stride byte
+// offset) and along m or n one 64 x 64 box apart (leading byte offset).
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kFBoxBytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+// fp32 tile added to global memory by the TMA unit (each element once: the order is fixed).
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+struct Unit {
+  int prob, m, n, split;
+};
+
+// Unit `id` of the launch: its product, and within it the K split (fastest, so that the splits of a
+// tile share its operands' L2 lines in time) and the tile, walked in panels of kFfnRaster m-tiles.
+__device__ __forceinline__ Unit find_unit_ffn(const FfnParams& P, int id) {
+  Unit t;
+  t.prob = 0;
+#pragma unroll
+  for (int i = 1; i < kFfnMaxProblems; ++i)
+    if (i < P.nprob && id >= P.p[i].unit0) t.prob = i;
+  const FfnProblem& p = P.p[t.prob];
+  id -= p.unit0;
+  t.split = id % p.splits;
+  const int tile = id / p.splits;
+  const int per = kFfnRaster * p.nt;
+  const int first = tile / per * kFfnRaster, r = tile % per;
+  const int gm = min(kFfnRaster, p.mt - first);
+  t.m = first + r % gm;
+  t.n = r / gm;
+  return t;
+}
+
+__device__ __forceinline__ void split_range(const FfnProblem& p, int split, int& k0, int& k1) {
+  const int total = p.nkb * p.nseg;
+  k0 = (int)((int64_t)split * total / p.splits);
+  k1 = (int)((int64_t)(split + 1) * total / p.splits);
+}
+
+}  // namespace
+
+template <int kEpi>
+__global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnParams P) {
+  constexpr int kStagingTotal = staging_bytes(kEpi);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* staging = smem + (ring_bytes(kEpi) & ~1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStagingTotal);
+  uint64_t* empty = full + kFMaxStages;
+  uint64_t* acc_full = empty + kFMaxStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile uint32_t* s_peer_nfill = reinterpret_cast<volatile uint32_t*>(s_tmem + 2);
+  volatile int* s_go = reinterpret_cast<volatile int*>(s_tmem + 3);  // [2]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  DeviceMeta* meta = P.meta;
+  const int64_t limit = P.timeout_ns;
+  // one ring for the whole launch: its stage holds the largest product's operands
+  int stage_bytes = 0;
+  for (int i = 0; i < P.nprob; ++i) stage_bytes = max(stage_bytes, kFABytes + b_bytes(P.p[i].bn, P.p[i].b_mn));
+  stage_bytes = (stage_bytes + 1023) & ~1023;
+  const int nst = min(kFMaxStages, (ring_bytes(kEpi) & ~1023) / stage_bytes);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < nst; ++i) {
+      mbar_init(&full[i], 2);  // one arrival per producer (CTA 0's barrier is the one used)
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);  // 4 epilogue warps x 2 CTAs
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    *s_peer_nfill = 0;
+    fence_mbar_init();
+    for (int i = 0; i < P.nprob; ++i) {
+      tma_prefetch_desc(&P.p[i].a[0]);
+      tma_prefetch_desc(&P.p[i].b[P.p[i].b_by_rank ? rank : 0]);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(s_tmem), 2 * kAccCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  griddep_wait();
+  const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
+  const uint32_t acc_empty_c0 = mapa_shared(smem_u32(acc_empty), 0);
+  uint32_t nfill = 0;
+  bool mma_issued = false;
+
+  if (warp == 0) {
+    // ---------------------------------- producers ----------------------------------
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int id = pair; ok && id < P.units; id += npairs) {
+        const Unit t = find_unit_ffn(P, id);
+        const FfnProblem& p = P.p[t.prob];
+        int k0, k1;
+        split_range(p, t.split, k0, k1);
+        const int arow = t.m * kFfnTileM + (int)rank * 128;
+        const int half = p.bn / 2;
+        const int brow = p.b_by_rank ? t.n * half : t.n * p.bn + (int)rank * half;
+        const int bboxes = (half + 63) / 64;
+        const uint32_t bytes = kFABytes + b_bytes(p.bn, p.b_mn);
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!wait_bar(&empty[stage], phase ^ 1, meta, s_abort, limit, kSiteProducerEmpty)) { ok = false; break; }
+          const int seg = kb >= p.nkb ? 1 : 0;
+          const int k = (kb - seg * p.nkb) * kBK;
+          const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + kFABytes;
+          const uint32_t fb = full_c0 + 8u * stage;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          else mbar_arrive_expect_tx_cluster(fb, bytes);
+          const CUtensorMap* am = &p.a[seg];
+          const CUtensorMap* bm = &p.b[p.b_by_rank ? (int)rank : seg];
+          if (p.a_mn) {
+            tma_load_2d_pair(a, am, fb, arow, k);
+            tma_load_2d_pair(a + kFBoxBytes, am, fb, arow + 64, k);
+          } else {
+            tma_load_2d_pair(a, am, fb, k, arow);
+          }
+          if (p.b_mn) {
+            for (int j = 0; j < bboxes; ++j) tma_load_2d_pair(b + j * kFBoxBytes, bm, fb, brow + j * 64, k);
+          } else {
+            tma_load_2d_pair(b, bm, fb, k, brow);
+          }
+          ++nfill;
+          if (++stage == (uint32_t)nst) { stage = 0; phase ^= 1; }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer (CTA 0) ------------------------------
+    if (rank == 0 && lane == 0) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true;
+      for (int id = pair; ok && id < P.units; id += npairs) {
+        const Unit t = find_unit_ffn(P, id);
+        const FfnProblem& p = P.p[t.prob];
+        int k0, k1;
+        split_range(p, t.split, k0, k1);
+        const uint32_t idesc = idesc_bf16_f32(kFfnTileM, p.bn) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
+        // a 16-wide K step: 32 bytes further along a K-major row, two atoms along MN-major k
+        const uint64_t astep = p.a_mn ? (2048 >> 4) : (32 >> 4), bstep = p.b_mn ? (2048 >> 4) : (32 >> 4);
+        if (!wait_bar(&acc_empty[acc], acc_phase ^ 1, meta, s_abort, limit, kSiteMmaAcc)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * kAccCols;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!wait_bar(&full[stage], phase, meta, s_abort, limit, kSiteMmaFull)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + kFABytes;
+          const uint64_t ad = p.a_mn ? sdesc_mnmajor_sw128(a) : sdesc_kmajor_sw128(a);
+          const uint64_t bd = p.b_mn ? sdesc_mnmajor_sw128(b) : sdesc_kmajor_sw128(b);
+#pragma unroll
+          for (int kk = 0; kk < kBK / kUK; ++kk)
+            umma_bf16_pair(d, ad + kk * astep, bd + kk * bstep, idesc, (kb != k0) || kk != 0);
+          mma_issued = true;
+          umma_commit_pair_mc(&empty[stage], 3);
+          if (++stage == (uint32_t)nst) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        umma_commit_pair_mc(&acc_full[acc], 3);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------- epilogue -----------------------------------
+    // Each thread owns one row of the CTA's 128. A step takes 32 columns: bf16 results are staged
+    // as 64-byte rows (64-byte swizzle), fp32 ones as 128-byte rows, and stored by TMA.
+    const int q = warp & 3;
+    const int row = q * 32 + lane;
+    const bool leader = (warp == 2 && lane == 0);
+    uint32_t acc = 0, acc_phase = 0, sb = 0;
+    auto put_bf16 = [&](uint8_t* buf, const uint32_t (&w)[16]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(buf + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    };
+    auto put_f32 = [&](uint8_t* buf, const uint32_t (&w)[32]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(buf + row * 128 + ((j ^ (row & 7)) << 4)) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    };
+    uint32_t it = 0;
+    for (int id = pair; id < P.units; id += npairs, ++it) {
+      const Unit t = find_unit_ffn(P, id);
+      const FfnProblem& p = P.p[t.prob];
+      // one thread waits for the accumulator and tells the other 127, so that the warps always
+      // leave the loop together
+      if (leader) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
+      named_bar_sync(1, 128);
+      if (s_go[it & 1] == 0) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem_base + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
+      const int m0 = t.m * kFfnTileM + (int)rank * 128;
+      const int mstore = p.splits > 1 ? t.split * p.mpad + m0 : m0;
+      const bool rows_in = p.splits > 1 || m0 < p.nrows;  // partials hold whole tiles of rows
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_c0 + 8u * acc);
+      };
+      if (kEpi == kFfnStore || p.splits > 1) {
+        const int nchunk = p.bn / kFChunk;
+        // partials of u | g: the tile's second half belongs to g's columns
+        const int hn = p.bn / 2;
+#pragma unroll 1
+        for (int cc = 0; cc < nchunk; ++cc) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tacc + cc * kFChunk, v);
+          tmem_ld_wait();
+          if (cc == nchunk - 1) release();
+          uint8_t* buf = staging + sb * 16384;
+          if (leader) bulk_wait_group_read<1>();
+          named_bar_sync(1, 128);
+          if (p.out_kind == 0) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            put_bf16(buf, pk);
+          } else {
+            put_f32(buf, v);
+          }
+          fence_proxy_async_shared();
+          named_bar_sync(1, 128);
+          if (leader) {
+            int col = t.n * p.bn + cc * kFChunk;
+            bool in = rows_in && col < p.ncols;
+            if (p.b_by_rank) {
+              const int c = t.n * hn + (cc * kFChunk) % hn;
+              in = rows_in && c < p.ncols;
+              col = cc * kFChunk < hn ? c : p.gcol + c;
+            }
+            if (in) {
+              if (p.out_kind == 2) tma_reduce_add_2d(&p.out, smem_u32(buf), col, mstore);
+              else tma_store_2d(&p.out, smem_u32(buf), col, mstore);
+            }
+            bulk_commit_group();
+          }
+          sb ^= 1;
+        }
+      } else if constexpr (kEpi == kFfnSwiglu) {
+        const int hn = p.bn / 2, nchunk = hn / kFChunk;
+#pragma unroll 1
+        for (int cc = 0; cc < nchunk; ++cc) {
+          uint32_t u[32], g[32], pk[16];
+          tmem_ld_32x32b_x32(tacc + cc * kFChunk, u);
+          tmem_ld_32x32b_x32(tacc + hn + cc * kFChunk, g);
+          tmem_ld_wait();
+          if (cc == nchunk - 1) release();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            pk[j] = pack_bf16x2(swiglu(__uint_as_float(u[2 * j]), __uint_as_float(g[2 * j])),
+                                swiglu(__uint_as_float(u[2 * j + 1]), __uint_as_float(g[2 * j + 1])));
+          uint8_t* buf = staging + sb * 24576;
+          if (leader) bulk_wait_group_read<1>();
+          named_bar_sync(1, 128);
+          put_bf16(buf, pk);
+          if (P.save) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+            put_bf16(buf + 8192, pk);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+            put_bf16(buf + 16384, pk);
+          }
+          fence_proxy_async_shared();
+          named_bar_sync(1, 128);
+          if (leader) {
+            const int col = t.n * hn + cc * kFChunk;
+            if (rows_in && col < p.ncols) {
+              tma_store_2d(&p.out, smem_u32(buf), col, m0);
+              if (P.save) {
+                tma_store_2d(&P.out2, smem_u32(buf) + 8192, col, m0);
+                tma_store_2d(&P.out3, smem_u32(buf) + 16384, col, m0);
+              }
+            }
+            bulk_commit_group();
+          }
+          sb ^= 1;
+        }
+      } else if constexpr (kEpi == kFfnDSwiglu) {
+        const int nchunk = p.bn / kFChunk;
+        const bool mine = m0 + row < p.nrows;
+        const size_t base = (size_t)(mine ? m0 + row : 0) * p.ncols;
+        uint4 un[4], gn[4];
+        auto fetch = [&](int cc) {
+          const int col = t.n * p.bn + cc * kFChunk;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // ncols is a multiple of 8: a 16-byte vector is inside or outside as a whole
+            const bool in = mine && col + 8 * j < p.ncols;
+            un[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.u + base + col + 8 * j)) : make_uint4(0, 0, 0, 0);
+            gn[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.g + base + col + 8 * j)) : make_uint4(0, 0, 0, 0);
+          }
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int cc = 0; cc < nchunk; ++cc) {
+          uint32_t v[32], du[16], dg[16], hh[16];
+          tmem_ld_32x32b_x32(tacc + cc * kFChunk, v);
+          uint32_t uw[16], gw[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uw[4 * j] = un[j].x; uw[4 * j + 1] = un[j].y; uw[4 * j + 2] = un[j].z; uw[4 * j + 3] = un[j].w;
+            gw[4 * j] = gn[j].x; gw[4 * j + 1] = gn[j].y; gw[4 * j + 2] = gn[j].z; gw[4 * j + 3] = gn[j].w;
+          }
+          if (cc + 1 < nchunk) fetch(cc + 1);
+          tmem_ld_wait();
+          if (cc == nchunk - 1) release();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float a0, a1, b0, b1, c0, c1;
+            dswiglu(__uint_as_float(v[2 * j]), __uint_as_float(uw[j] << 16), __uint_as_float(gw[j] << 16), a0, b0, c0);
+            dswiglu(__uint_as_float(v[2 * j + 1]), __uint_as_float(uw[j] & 0xffff0000u),
+                    __uint_as_float(gw[j] & 0xffff0000u), a1, b1, c1);
+            du[j] = pack_bf16x2(a0, a1);
+            dg[j] = pack_bf16x2(b0, b1);
+            hh[j] = pack_bf16x2(c0, c1);
+          }
+          uint8_t* buf = staging + sb * 24576;
+          if (leader) bulk_wait_group_read<1>();
+          named_bar_sync(1, 128);
+          put_bf16(buf, du);
+          put_bf16(buf + 8192, dg);
+          put_bf16(buf + 16384, hh);
+          fence_proxy_async_shared();
+          named_bar_sync(1, 128);
+          if (leader) {
+            const int col = t.n * p.bn + cc * kFChunk;
+            if (rows_in && col < p.ncols) {
+              tma_store_2d(&p.out, smem_u32(buf), col, m0);
+              tma_store_2d(&P.out2, smem_u32(buf) + 8192, col, m0);
+              tma_store_2d(&P.out3, smem_u32(buf) + 16384, col, m0);
+            }
+            bulk_commit_group();
+          }
+          sb ^= 1;
+        }
+      }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+    }
+    if (leader) bulk_wait_group<0>();
+  }
+
+  griddep_launch_dependents();
+  // teardown: every fill of either CTA completes on CTA 0's `full` barriers, and every MMA writes
+  // both CTAs' tensor memory, so CTA 0 drains both before either CTA moves on
+  tc_fence_before();
+  if (rank == 1 && threadIdx.x == 0) st_cluster_u32(mapa_shared(smem_u32((const void*)s_peer_nfill), 0), nfill);
+  cluster_sync_all();
+  if (rank == 0 && threadIdx.x == 0) {
+    // after an abort one producer may have issued up to a ring's worth of fills that the other did
+    // not: arrive for the missing producer so that those phases complete when the bytes land
+    const uint32_t np = *s_peer_nfill;
+    const uint32_t lo = min(nfill, np), hi = max(nfill, np);
+    for (uint32_t i = lo; i < hi && i < lo + nst; ++i) mbar_arrive(&full[i % nst]);
+    drain_fills(full, nst, hi, meta, limit);
+  }
+  if (rank == 0 && threadIdx.x == 32 && mma_issued) {
+    umma_commit_pair(drain);
+    wait_bar_drain(drain, 0, meta, limit);
+  }
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * kAccCols);
+}
+
+namespace {
+
+// 8 consecutive elements of the sum of the splits' partials, in split order.
+__device__ __forceinline__ void sum_parts(const FfnReduce& r, int64_t off, float (&a)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = 0.f;
+  for (int s = 0; s < r.splits; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(r.parts + s * r.split_stride + off);
+    const float4 x = __ldcg(p), y = __ldcg(p + 1);
+    a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+    a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint16_t* p, float (&a)[8]) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = 0.f;
+  add_bf16x8(a, v);
+}
+
+}  // namespace
+
+// One thread per 8 columns (every N here is a multiple of 8).
+template <int kEpi>
+__global__ void __launch_bounds__(256) ffn_reduce_kernel(const FfnReduce r) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int vec = r.cols / 8;
+  const int64_t n = (int64_t)r.rows * vec;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / vec;
+    const int col = (int)(i % vec) * 8;
+    const int64_t o = row * r.cols + col;
+    float a[8];
+    sum_parts(r, row * r.ld + col, a);
+    if constexpr (kEpi == kFfnStore) {
+      if (r.out_kind == 0) {
+        store8<true>(r.out, o, a);
+      } else {
+        if (r.out_kind == 2) {
+          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(r.out) + o);
+          const float4 x = p[0], y = p[1];
+          a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+          a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+        }
+        store8<false>(r.out, o, a);
+      }
+    } else if constexpr (kEpi == kFfnSwiglu) {
+      float g[8], h[8];
+      sum_parts(r, row * r.ld + r.gcol + col, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = swiglu(a[j], g[j]);
+      store8<true>(r.out, o, h);
+      if (r.out2) {
+        store8<true>(r.out2, o, a);
+        store8<true>(r.out3, o, g);
+      }
+    } else {
+      float u[8], g[8], du[8], dg[8], h[8];
+      unpack8(r.u + o, u);
+      unpack8(r.g + o, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dswiglu(a[j], u[j], g[j], du[j], dg[j], h[j]);
+      store8<true>(r.out, o, du);
+      store8<true>(r.out2, o, dg);
+      store8<true>(r.out3, o, h);
+    }
+  }
+}
+
+cudaError_t launch_ffn_reduce(const FfnReduce& r, int epilogue, int num_sms, cudaStream_t stream) {
+  const int64_t n = (int64_t)r.rows * (r.cols / 8);
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, (int64_t)num_sms * 8));
+  auto* k = epilogue == kFfnStore ? ffn_reduce_kernel<kFfnStore>
+                                  : (epilogue == kFfnSwiglu ? ffn_reduce_kernel<kFfnSwiglu> : ffn_reduce_kernel<kFfnDSwiglu>);
+  return launch_k(k, dim3(grid), dim3(256), 0, stream, r);
+}
+
+namespace {
+
+typedef void (*FfnKernel)(const FfnParams);
+
+FfnKernel ffn_kernel(int epilogue) {
+  return epilogue == kFfnStore ? ffn_gemm_kernel<kFfnStore>
+                               : (epilogue == kFfnSwiglu ? ffn_gemm_kernel<kFfnSwiglu> : ffn_gemm_kernel<kFfnDSwiglu>);
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_gemm(const FfnParams& p, int epilogue, int pairs, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * std::min(pairs, p.units));
+  cfg.blockDim = dim3(kFThreads);
+  cfg.dynamicSmemBytes = kFSmem + 1024;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, ffn_kernel(epilogue), p);
+}
+
+// Sets the kernels' shared-memory limits and returns how many 2-CTA clusters fit on the device at
+// once (0 if none).
+cudaError_t configure_ffn_kernels(int* max_pairs) {
+  *max_pairs = 0;
+  for (int e = 0; e < 3; ++e) {
+    const cudaError_t rc = cudaFuncSetAttribute(ffn_kernel(e), cudaFuncAttributeMaxDynamicSharedMemorySize, kFSmem + 1024);
+    if (rc != cudaSuccess) return rc;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kFThreads);
+  cfg.dynamicSmemBytes = kFSmem + 1024;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(max_pairs, (void*)ffn_kernel(kFfnStore), &cfg);
+}
+
+}  // namespace moe

@@ -36,6 +36,9 @@ MOE_FLAG_UNFUSED_SMALL = 1024
 MOE_FLAG_TWO_TILES = 2048
 MOE_FLAG_TRACE = 4
 
+MOE_FFN_GRAD_F32 = 1
+MOE_FFN_GRAD_ADD = 2
+
 
 class moe_config(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32),
@@ -58,6 +61,10 @@ class moe_mxfp8_experts(ctypes.Structure):
     _fields_ = [(n, moe_mxfp8_mat) for n in ("up", "gate", "down", "shared_up", "shared_gate", "shared_down")]
 
 
+class moe_ffn_grads(ctypes.Structure):
+    _fields_ = [("up", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("down", ctypes.c_void_p)]
+
+
 # every symbol the header declares, with its C signature
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 SIGNATURES = {
@@ -74,6 +81,11 @@ SIGNATURES = {
     "moe_mxfp8_scale_bytes": (_I64, [_I64, _I64]),
     "moe_quantize_mxfp8": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P]),
     "moe_forward_mxfp8": (ctypes.c_int, [_P, _P, _I32, _P, _P, ctypes.POINTER(moe_mxfp8_experts), _I32, _P, _P]),
+    "moe_ffn_workspace_bytes": (_I64, [_I64, _I32, _I32, _I32]),
+    "moe_ffn_forward": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, ctypes.POINTER(moe_shared_w), _P, _I32, _P, _P,
+                                       _P, _I64, _P]),
+    "moe_ffn_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I32, _I32, ctypes.POINTER(moe_shared_w), _P,
+                                        ctypes.POINTER(moe_ffn_grads), ctypes.c_uint32, _P, _I64, _P]),
     "moe_router_logits": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P]),
     "moe_gate_topk": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P]),
     "moe_align_block_size": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _P]),
@@ -137,10 +149,26 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
+    s = torch.cuda.current_stream(device) if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _is_tensor(t, name, shape, dtypes, device=None):
+    """Raises unless t is a contiguous CUDA tensor of this shape and one of these dtypes, on
+    `device` (None: any). The library sees only its address."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    if str(t.dtype).split(".")[-1] not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device.type != "cuda" or (device is not None and t.device.index != device):
+        raise ValueError(f"{name} must be on {'CUDA' if device is None else f'cuda:{device}'}, got {t.device}")
 
 
 class MoELayer:
@@ -215,6 +243,93 @@ class MoELayer:
                                          top_k or self.cfg.top_k, _ptr(out_host), _stream(stream)),
               "moe_forward_host_async")
         return out_host
+
+    # ---- the gated feed-forward block ----
+    def _ffn_sizes(self, x, wts, device):
+        """(T, H, D) of a block's call, its input and weights checked."""
+        names = ("Ws_up", "Ws_gate", "Ws_down")
+        for n in names:
+            if wts.get(n) is None:
+                raise ValueError(f"the block needs {n}")
+        if getattr(wts["Ws_up"], "ndim", 0) != 2 or getattr(x, "ndim", 0) != 2:
+            raise ValueError("x must be [T, H] and Ws_up [D, H]")
+        (T, H), D = x.shape, wts["Ws_up"].shape[0]
+        _is_tensor(x, "x", (T, H), ("bfloat16",), device)
+        for n, shape in zip(names, ((D, H), (D, H), (H, D))):
+            _is_tensor(wts[n], n, shape, ("bfloat16",), device)
+        return T, H, D
+
+    def _ffn_workspace(self, workspace, sizes, backward, device, stream):
+        """The caller's workspace, or one for this call alone (allocated in the order of the
+        call's stream, so that its memory is reused only behind the call)."""
+        import torch
+        need = lib.moe_ffn_workspace_bytes(*sizes, backward)
+        if need < 0:
+            raise ValueError(f"the block takes multiples of 8 for its hidden and inner size, got {sizes[1]} and {sizes[2]}")
+        if workspace is None:
+            with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}")
+        elif workspace.numel() < need:
+            raise ValueError(f"the workspace needs {need} bytes, got {workspace.numel()}")
+        else:
+            _is_tensor(workspace, "workspace", workspace.shape, ("uint8",), device)
+        return workspace
+
+    @staticmethod
+    def ffn_workspace_bytes(T, hidden, inter, backward=False):
+        """Bytes of the workspace of ffn_forward or ffn_backward (a uint8 tensor)."""
+        n = lib.moe_ffn_workspace_bytes(T, hidden, inter, 1 if backward else 0)
+        if n < 0:
+            raise ValueError(f"the block takes multiples of 8 for its hidden and inner size, got {hidden} and {inter}")
+        return n
+
+    def ffn_forward(self, x, wts, out, u=None, g=None, workspace=None, stream=None):
+        """moe_ffn_forward: out = W_down (SiLU(W_up x) * (W_gate x)) with wts["Ws_up"] and
+        wts["Ws_gate"] [D, H] and wts["Ws_down"] [H, D]; x [T, H] bf16, out [T, H] bf16 or fp32.
+        u and g ([T, D] bf16, both or neither) receive the pre-activations for ffn_backward."""
+        dev = self.query(13)
+        T, H, D = self._ffn_sizes(x, wts, dev)
+        _is_tensor(out, "out", (T, H), ("bfloat16", "float32"), dev)
+        if (u is None) != (g is None):
+            raise ValueError("u and g go together")
+        for t, n in ((u, "u"), (g, "g")):
+            if t is not None:
+                _is_tensor(t, n, (T, D), ("bfloat16",), dev)
+        ws = self._ffn_workspace(workspace, (T, H, D), 0, dev, stream)
+        sh = self._shared(wts)
+        check(lib.moe_ffn_forward(self.h, _ptr(x), T, H, D, sh[0], _ptr(out), 1 if out.element_size() == 2 else 0,
+                                  _ptr(u), _ptr(g), _ptr(ws), ws.numel(), _stream(stream, dev)), "moe_ffn_forward")
+        return out
+
+    def ffn_backward(self, dout, x, u, g, wts, grads, accumulate=False, workspace=None, stream=None):
+        """moe_ffn_backward: fills grads["x"] ([T, H] bf16) and grads["Ws_up"], grads["Ws_gate"],
+        grads["Ws_down"] (shaped as the weights, all bf16 or all fp32; with accumulate, fp32 and
+        added to). A gradient that grads lacks, or has as None, is not computed."""
+        dev = self.query(13)
+        T, H, D = self._ffn_sizes(x, wts, dev)
+        _is_tensor(dout, "dout", (T, H), ("bfloat16",), dev)
+        for t, n in ((u, "u"), (g, "g")):
+            _is_tensor(t, n, (T, D), ("bfloat16",), dev)
+        unknown = set(grads) - {"x", "Ws_up", "Ws_gate", "Ws_down"}
+        if unknown:
+            raise ValueError(f"no gradient named {sorted(unknown)}")
+        if grads.get("x") is not None:
+            _is_tensor(grads["x"], "grads['x']", (T, H), ("bfloat16",), dev)
+        dw = {n: grads.get(n) for n in ("Ws_up", "Ws_gate", "Ws_down")}
+        kinds = {str(t.dtype).split(".")[-1] for t in dw.values() if t is not None}
+        for n, t in dw.items():
+            if t is not None:
+                _is_tensor(t, f"grads[{n!r}]", wts[n].shape, ("float32",) if accumulate else ("bfloat16", "float32"), dev)
+        if len(kinds) > 1:
+            raise TypeError("the weight gradients must all be bfloat16 or all float32")
+        flags = (MOE_FFN_GRAD_F32 if kinds == {"float32"} else 0) | (MOE_FFN_GRAD_ADD if accumulate and kinds else 0)
+        ws = self._ffn_workspace(workspace, (T, H, D), 1, dev, stream)
+        sh = self._shared(wts)
+        gr = moe_ffn_grads(*(None if t is None else t.data_ptr() for t in dw.values()))
+        check(lib.moe_ffn_backward(self.h, _ptr(dout), _ptr(x), _ptr(u), _ptr(g), T, H, D, sh[0],
+                                   _ptr(grads.get("x")), ctypes.byref(gr), flags, _ptr(ws), ws.numel(),
+                                   _stream(stream, dev)), "moe_ffn_backward")
+        return grads
 
     # ---- MXFP8 experts ----
     def quantize_mxfp8(self, src, stream=None):
