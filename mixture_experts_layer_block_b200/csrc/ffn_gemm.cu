@@ -20,7 +20,8 @@
 // K is split; the partial sums go to a workspace in fp32 and ffn_reduce_kernel adds them in split
 // order, so that results do not depend on timing.
 //
-// Warp roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (CTA 0), warps 2-5 epilogue.
+// Warp roles per CTA: warps 0 and 6 TMA producers (A and B), warp 1 MMA issuer (CTA 0), warps 2-5
+// epilogue.
 #include <algorithm>
 
 #include "ffn.cuh"
@@ -30,7 +31,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kFThreads = 192;
+constexpr int kFThreads = 224;
 constexpr int kFMaxStages = 8;
 constexpr int kFABytes = 128 * kBK * 2;  // 16 KB of A per CTA and stage
 constexpr int kFBoxBytes = 64 * 64 * 2;  // an MN-major box of 64 x 64
@@ -61,6 +62,22 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32
                    reinterpret_cast<uint64_t>(map)),
                "r"(src), "r"(c0), "r"(c1)
                : "memory");
+}
+
+// One lane of a converged warp, chosen by the hardware. Unlike a test of the lane's number this
+// tells the compiler that what follows runs in one lane, so that the TMA and MMA instructions,
+// whose operands live in the warp's uniform registers, need no loop over the active lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// wait_bar with the first probe inline: most waits find their phase complete.
+__device__ __forceinline__ bool wait_bar_fast(uint64_t* bar, uint32_t parity, DeviceMeta* meta, volatile int* s_abort,
+                                              int64_t limit, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_bar(bar, parity, meta, s_abort, limit, site);
 }
 
 struct Unit {
@@ -108,8 +125,8 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   uint64_t* drain = acc_empty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  volatile uint32_t* s_peer_nfill = reinterpret_cast<volatile uint32_t*>(s_tmem + 2);
-  volatile int* s_go = reinterpret_cast<volatile int*>(s_tmem + 3);  // [2]
+  volatile int* s_go = reinterpret_cast<volatile int*>(s_tmem + 2);           // [2]
+  volatile uint32_t* s_nfill = reinterpret_cast<volatile uint32_t*>(s_tmem + 4);  // [4] fills per producer
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -124,7 +141,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < nst; ++i) {
-      mbar_init(&full[i], 2);  // one arrival per producer (CTA 0's barrier is the one used)
+      mbar_init(&full[i], 4);  // one arrival per producer (CTA 0's barrier is the one used)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -133,7 +150,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     }
     mbar_init(drain, 1);
     *s_abort = 0;
-    *s_peer_nfill = 0;
+    for (int i = 0; i < 4; ++i) s_nfill[i] = 0;
     fence_mbar_init();
     for (int i = 0; i < P.nprob; ++i) {
       tma_prefetch_desc(&P.p[i].a[0]);
@@ -154,41 +171,46 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   uint32_t nfill = 0;
   bool mma_issued = false;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 6) {
     // ---------------------------------- producers ----------------------------------
-    if (lane == 0) {
+    // Warp 0 loads this CTA's rows of A, warp 6 its rows of B: a stage has up to four TMA
+    // instructions, and one thread that issued them all fell behind the tensor cores.
+    const bool is_a = warp == 0;
+    if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
+      const uint32_t ring = smem_u32(smem) + (is_a ? 0 : kFABytes);
       for (int id = pair; ok && id < P.units; id += npairs) {
         const Unit t = find_unit_ffn(P, id);
         const FfnProblem& p = P.p[t.prob];
         int k0, k1;
         split_range(p, t.split, k0, k1);
-        const int arow = t.m * kFfnTileM + (int)rank * 128;
         const int half = p.bn / 2;
-        const int brow = p.b_by_rank ? t.n * half : t.n * p.bn + (int)rank * half;
-        const int bboxes = (half + 63) / 64;
-        const uint32_t bytes = kFABytes + b_bytes(p.bn, p.b_mn);
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!wait_bar(&empty[stage], phase ^ 1, meta, s_abort, limit, kSiteProducerEmpty)) { ok = false; break; }
-          const int seg = kb >= p.nkb ? 1 : 0;
-          const int k = (kb - seg * p.nkb) * kBK;
-          const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + kFABytes;
+        const bool mn = is_a ? p.a_mn : p.b_mn;
+        const int row = is_a ? t.m * kFfnTileM + (int)rank * 128
+                             : (p.b_by_rank ? t.n * half : t.n * p.bn + (int)rank * half);
+        const bool two = mn && (is_a || half > 64);
+        const uint32_t bytes = is_a ? kFABytes : b_bytes(p.bn, p.b_mn);
+        const CUtensorMap* maps = is_a ? p.a : p.b;
+        int seg = k0 >= p.nkb ? 1 : 0;
+        int left = p.nkb * (seg + 1) - k0;
+        int k = (k0 - seg * p.nkb) * kBK;
+        const CUtensorMap* map = &maps[!is_a && p.b_by_rank ? (int)rank : seg];
+        for (int n = k1 - k0; n > 0; --n) {
+          if (!wait_bar_fast(&empty[stage], phase ^ 1, meta, s_abort, limit, kSiteProducerEmpty)) { ok = false; break; }
+          const uint32_t dst = ring + stage * stage_bytes;
           const uint32_t fb = full_c0 + 8u * stage;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
-          else mbar_arrive_expect_tx_cluster(fb, bytes);
-          const CUtensorMap* am = &p.a[seg];
-          const CUtensorMap* bm = &p.b[p.b_by_rank ? (int)rank : seg];
-          if (p.a_mn) {
-            tma_load_2d_pair(a, am, fb, arow, k);
-            tma_load_2d_pair(a + kFBoxBytes, am, fb, arow + 64, k);
+          mbar_arrive_expect_tx_cluster(fb, bytes);
+          if (mn) {
+            tma_load_2d_pair(dst, map, fb, row, k);
+            if (two) tma_load_2d_pair(dst + kFBoxBytes, map, fb, row + 64, k);
           } else {
-            tma_load_2d_pair(a, am, fb, k, arow);
+            tma_load_2d_pair(dst, map, fb, k, row);
           }
-          if (p.b_mn) {
-            for (int j = 0; j < bboxes; ++j) tma_load_2d_pair(b + j * kFBoxBytes, bm, fb, brow + j * 64, k);
-          } else {
-            tma_load_2d_pair(b, bm, fb, k, brow);
+          k += kBK;
+          if (--left == 0) {  // the second segment's operands
+            k = 0;
+            map = &maps[!is_a && p.b_by_rank ? (int)rank : 1];
           }
           ++nfill;
           if (++stage == (uint32_t)nst) { stage = 0; phase ^= 1; }
@@ -196,9 +218,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       }
     }
     __syncwarp();
+    nfill = __reduce_max_sync(0xffffffffu, nfill);  // every lane: what the elected one counted
   } else if (warp == 1) {
     // ------------------------------ MMA issuer (CTA 0) ------------------------------
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (int id = pair; ok && id < P.units; id += npairs) {
@@ -213,7 +236,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         tc_fence_after();
         const uint32_t d = tmem_base + acc * kAccCols;
         for (int kb = k0; kb < k1; ++kb) {
-          if (!wait_bar(&full[stage], phase, meta, s_abort, limit, kSiteMmaFull)) { ok = false; break; }
+          if (!wait_bar_fast(&full[stage], phase, meta, s_abort, limit, kSiteMmaFull)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + kFABytes;
           const uint64_t ad = p.a_mn ? sdesc_mnmajor_sw128(a) : sdesc_kmajor_sw128(a);
@@ -417,17 +440,19 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   // teardown: every fill of either CTA completes on CTA 0's `full` barriers, and every MMA writes
   // both CTAs' tensor memory, so CTA 0 drains both before either CTA moves on
   tc_fence_before();
-  if (rank == 1 && threadIdx.x == 0) st_cluster_u32(mapa_shared(smem_u32((const void*)s_peer_nfill), 0), nfill);
+  if (lane == 0 && (warp == 0 || warp == 6))
+    st_cluster_u32(mapa_shared(smem_u32((const void*)&s_nfill[2 * rank + (warp == 6 ? 1 : 0)]), 0), nfill);
   cluster_sync_all();
   if (rank == 0 && threadIdx.x == 0) {
-    // after an abort one producer may have issued up to a ring's worth of fills that the other did
-    // not: arrive for the missing producer so that those phases complete when the bytes land
-    const uint32_t np = *s_peer_nfill;
-    const uint32_t lo = min(nfill, np), hi = max(nfill, np);
-    for (uint32_t i = lo; i < hi && i < lo + nst; ++i) mbar_arrive(&full[i % nst]);
+    // after an abort some producers may have issued up to a ring's worth of fills that others did
+    // not: arrive for those so that the phases complete when the bytes land
+    uint32_t hi = 0;
+    for (int i = 0; i < 4; ++i) hi = max(hi, s_nfill[i]);
+    for (int i = 0; i < 4; ++i)
+      for (uint32_t j = s_nfill[i]; j < hi; ++j) mbar_arrive(&full[j % nst]);
     drain_fills(full, nst, hi, meta, limit);
   }
-  if (rank == 0 && threadIdx.x == 32 && mma_issued) {
+  if (mma_issued) {  // in the thread that issued the MMAs
     umma_commit_pair(drain);
     wait_bar_drain(drain, 0, meta, limit);
   }
