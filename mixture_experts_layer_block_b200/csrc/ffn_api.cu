@@ -30,14 +30,15 @@ void shape_product(Product& p, int bn, int splits) {
   const int cols = p.dual ? bn / 2 : bn;
   p.nt = (int)((p.N + cols - 1) / cols);
   p.splits = splits;
-  // a stored chunk is 32 columns wide: g's part starts on a whole chunk, past u's last one
-  p.part_ld = p.dual ? 2 * round_up(p.N, 32) : p.N;
+  // a stored chunk is 32 columns wide and may start at any multiple of 16 below N: g's part starts
+  // past the end of u's last chunk
+  p.part_ld = p.dual ? 2 * (round_up(p.N, 16) + 32) : p.N;
   p.part_bytes = splits > 1 ? (int64_t)splits * p.mt * kFfnTileM * p.part_ld * 4 : 0;
 }
 
 // Picks the tile width and the K splits of one launch's products by an estimate in SM clocks:
 //  - a 64-wide K block of a 256 x bn tile takes 2 * bn clocks of the pair's tensor cores (4096 MACs
-//    an SM and clock), but no less than its operands need to arrive (300);
+//    an SM and clock), but no less than one round of the ring's barriers (420);
 //  - a unit's fill and drain that nothing overlaps takes about 2500;
 //  - with more than one unit a pair, the last round is as long as a full one;
 //  - partial sums cost a second launch (about 6000) and their bytes, written and read once.
@@ -51,14 +52,14 @@ void plan(Product* p, int n) {
     dual = dual || p[i].dual;
     most = std::max(most, p[i].nkb);
   }
-  for (int bn = 128; bn <= 256; bn += dual ? 64 : 32) {
+  for (int bn = 128; bn <= 256; bn += dual ? 32 : 16) {
     for (int L = most; L >= 4 || L == most; L = L / 2) {
       double total = 0, longest = 0, parts = 0;
       int64_t units = 0;
       for (int i = 0; i < n; ++i) {
         const int s = std::min(16, (p[i].nkb + L - 1) / L);
         shape_product(p[i], bn, s);
-        const double kb = (double)((p[i].nkb + s - 1) / s) * std::max(2.0 * bn, 300.0) + 4.0 * bn;
+        const double kb = (double)((p[i].nkb + s - 1) / s) * std::max(2.0 * bn, 420.0) + 4.0 * bn;
         const int64_t u = (int64_t)p[i].mt * p[i].nt * s;
         units += u;
         total += kb * u;

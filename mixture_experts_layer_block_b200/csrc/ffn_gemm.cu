@@ -104,6 +104,10 @@ __device__ __forceinline__ Unit find_unit_ffn(const FfnParams& P, int id) {
   return t;
 }
 
+// First column of a tile's chunk `cc`. A width that is an odd multiple of 16 ends in a chunk that
+// overlaps the one before it by 16 columns: they are stored twice, with the same values.
+__device__ __forceinline__ int chunk_col(int cc, int width) { return min(cc * kFChunk, width - kFChunk); }
+
 __device__ __forceinline__ void split_range(const FfnProblem& p, int split, int& k0, int& k1) {
   const int total = p.nkb * p.nseg;
   k0 = (int)((int64_t)split * total / p.splits);
@@ -278,6 +282,24 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     for (int id = pair; id < P.units; id += npairs, ++it) {
       const Unit t = find_unit_ffn(P, id);
       const FfnProblem& p = P.p[t.prob];
+      const int m0 = t.m * kFfnTileM + (int)rank * 128;
+      // dh: a chunk of this row's u and g, requested a chunk ahead (the first before the wait)
+      const bool mine = kEpi == kFfnDSwiglu && m0 + row < p.nrows;
+      uint4 un[4], gn[4];
+      auto fetch = [&](int cc) {
+        const int col = t.n * p.bn + chunk_col(cc, p.bn);
+        const size_t base = (size_t)(mine ? m0 + row : 0) * p.ncols + col;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // ncols is a multiple of 8: a 16-byte vector is inside or outside as a whole
+          const bool in = mine && col + 8 * j < p.ncols;
+          un[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.u + base + 8 * j)) : make_uint4(0, 0, 0, 0);
+          gn[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.g + base + 8 * j)) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      if constexpr (kEpi == kFfnDSwiglu) {
+        if (p.splits == 1) fetch(0);
+      }
       // one thread waits for the accumulator and tells the other 127, so that the warps always
       // leave the loop together
       if (leader) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
@@ -285,7 +307,6 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       if (s_go[it & 1] == 0) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
-      const int m0 = t.m * kFfnTileM + (int)rank * 128;
       const int mstore = p.splits > 1 ? t.split * p.mpad + m0 : m0;
       const bool rows_in = p.splits > 1 || m0 < p.nrows;  // partials hold whole tiles of rows
       auto release = [&]() {
@@ -294,18 +315,24 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         if (lane == 0) mbar_arrive_cluster(acc_empty_c0 + 8u * acc);
       };
       if (kEpi == kFfnStore || p.splits > 1) {
-        const int nchunk = p.bn / kFChunk;
         // partials of u | g: the tile's second half belongs to g's columns
-        const int hn = p.bn / 2;
+        const int width = p.b_by_rank ? p.bn / 2 : p.bn, per = (width + kFChunk - 1) / kFChunk;
+        const int nchunk = p.b_by_rank ? 2 * per : per;
 #pragma unroll 1
         for (int cc = 0; cc < nchunk; ++cc) {
+          const int part = cc >= per ? 1 : 0;
+          const int c0 = chunk_col(cc - part * per, width);
           uint32_t v[32];
-          tmem_ld_32x32b_x32(tacc + cc * kFChunk, v);
+          tmem_ld_32x32b_x32(tacc + part * width + c0, v);
           tmem_ld_wait();
           if (cc == nchunk - 1) release();
           uint8_t* buf = staging + sb * 16384;
           if (leader) bulk_wait_group_read<1>();
           named_bar_sync(1, 128);
+          if (p.out_kind == 2 && c0 < cc * kFChunk) {  // columns that the chunk before has added
+#pragma unroll
+            for (int j = 0; j < kFChunk / 2; ++j) v[j] = 0;
+          }
           if (p.out_kind == 0) {
             uint32_t pk[16];
 #pragma unroll
@@ -317,13 +344,8 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           fence_proxy_async_shared();
           named_bar_sync(1, 128);
           if (leader) {
-            int col = t.n * p.bn + cc * kFChunk;
-            bool in = rows_in && col < p.ncols;
-            if (p.b_by_rank) {
-              const int c = t.n * hn + (cc * kFChunk) % hn;
-              in = rows_in && c < p.ncols;
-              col = cc * kFChunk < hn ? c : p.gcol + c;
-            }
+            const int c = t.n * width + c0, col = part * p.gcol + c;
+            const bool in = rows_in && c < p.ncols;
             if (in) {
               if (p.out_kind == 2) tma_reduce_add_2d(&p.out, smem_u32(buf), col, mstore);
               else tma_store_2d(&p.out, smem_u32(buf), col, mstore);
@@ -333,12 +355,13 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           sb ^= 1;
         }
       } else if constexpr (kEpi == kFfnSwiglu) {
-        const int hn = p.bn / 2, nchunk = hn / kFChunk;
+        const int hn = p.bn / 2, nchunk = (hn + kFChunk - 1) / kFChunk;
 #pragma unroll 1
         for (int cc = 0; cc < nchunk; ++cc) {
+          const int c0 = chunk_col(cc, hn);
           uint32_t u[32], g[32], pk[16];
-          tmem_ld_32x32b_x32(tacc + cc * kFChunk, u);
-          tmem_ld_32x32b_x32(tacc + hn + cc * kFChunk, g);
+          tmem_ld_32x32b_x32(tacc + c0, u);
+          tmem_ld_32x32b_x32(tacc + hn + c0, g);
           tmem_ld_wait();
           if (cc == nchunk - 1) release();
 #pragma unroll
@@ -360,7 +383,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           fence_proxy_async_shared();
           named_bar_sync(1, 128);
           if (leader) {
-            const int col = t.n * hn + cc * kFChunk;
+            const int col = t.n * hn + c0;
             if (rows_in && col < p.ncols) {
               tma_store_2d(&p.out, smem_u32(buf), col, m0);
               if (P.save) {
@@ -373,25 +396,12 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           sb ^= 1;
         }
       } else if constexpr (kEpi == kFfnDSwiglu) {
-        const int nchunk = p.bn / kFChunk;
-        const bool mine = m0 + row < p.nrows;
-        const size_t base = (size_t)(mine ? m0 + row : 0) * p.ncols;
-        uint4 un[4], gn[4];
-        auto fetch = [&](int cc) {
-          const int col = t.n * p.bn + cc * kFChunk;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // ncols is a multiple of 8: a 16-byte vector is inside or outside as a whole
-            const bool in = mine && col + 8 * j < p.ncols;
-            un[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.u + base + col + 8 * j)) : make_uint4(0, 0, 0, 0);
-            gn[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.g + base + col + 8 * j)) : make_uint4(0, 0, 0, 0);
-          }
-        };
-        fetch(0);
+        const int nchunk = (p.bn + kFChunk - 1) / kFChunk;
 #pragma unroll 1
         for (int cc = 0; cc < nchunk; ++cc) {
+          const int c0 = chunk_col(cc, p.bn);
           uint32_t v[32], du[16], dg[16], hh[16];
-          tmem_ld_32x32b_x32(tacc + cc * kFChunk, v);
+          tmem_ld_32x32b_x32(tacc + c0, v);
           uint32_t uw[16], gw[16];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -420,7 +430,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           fence_proxy_async_shared();
           named_bar_sync(1, 128);
           if (leader) {
-            const int col = t.n * p.bn + cc * kFChunk;
+            const int col = t.n * p.bn + c0;
             if (rows_in && col < p.ncols) {
               tma_store_2d(&p.out, smem_u32(buf), col, m0);
               tma_store_2d(&P.out2, smem_u32(buf) + 8192, col, m0);

@@ -8,6 +8,7 @@ is missing this module raises on import.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -149,26 +150,56 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream, device=None):
+def _stream(stream):
     import torch
-    s = torch.cuda.current_stream(device) if stream is None else stream
+    s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _is_tensor(t, name, shape, dtypes, device=None):
-    """Raises unless t is a contiguous CUDA tensor of this shape and one of these dtypes, on
-    `device` (None: any). The library sees only its address."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+def _is_tensor(t, name, shape, dtypes, device):
+    """Raises unless t is a contiguous CUDA tensor of this shape and one of these dtypes (names)
+    on this device: the library sees only its address."""
+    # the common case first, in as few attribute reads as it takes: a small call is as long as its checks
+    if isinstance(t, _tensor()) and t.dtype in _dtypes(dtypes) and t.shape == shape and t.is_contiguous() \
+            and t.is_cuda and t.get_device() == device:
+        return
+    if not isinstance(t, _tensor()):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
-    if str(t.dtype).split(".")[-1] not in dtypes:
+    if t.dtype not in _dtypes(dtypes):
         raise TypeError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device.type != "cuda" or (device is not None and t.device.index != device):
-        raise ValueError(f"{name} must be on {'CUDA' if device is None else f'cuda:{device}'}, got {t.device}")
+    raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+
+
+@functools.lru_cache(maxsize=None)
+def _tensor():
+    import torch
+    return torch.Tensor
+
+
+@functools.lru_cache(maxsize=None)
+def _dtypes(names):
+    import torch
+    return tuple(getattr(torch, n) for n in names)
+
+
+_BF16, _F32, _U8 = ("bfloat16",), ("float32",), ("uint8",)
+_BF16_F32 = ("bfloat16", "float32")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    """The cudaStream_t of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 class MoELayer:
@@ -184,6 +215,7 @@ class MoELayer:
         h = ctypes.c_void_p()
         check(lib.moe_init(ctypes.byref(self.cfg), ctypes.byref(h)), "moe_init")
         self.h = h
+        self.device = self.query(13)
         self.out_dtype = "bfloat16" if flags & MOE_FLAG_OUT_BF16 else "float32"
 
     def _check_out(self, out):
@@ -245,90 +277,88 @@ class MoELayer:
         return out_host
 
     # ---- the gated feed-forward block ----
-    def _ffn_sizes(self, x, wts, device):
-        """(T, H, D) of a block's call, its input and weights checked."""
-        names = ("Ws_up", "Ws_gate", "Ws_down")
-        for n in names:
-            if wts.get(n) is None:
-                raise ValueError(f"the block needs {n}")
-        if getattr(wts["Ws_up"], "ndim", 0) != 2 or getattr(x, "ndim", 0) != 2:
+    def _ffn_call(self, x, wts):
+        """(T, H, D, the C struct of the weights) of a block's call, its input and weights checked."""
+        up, gate, down = wts.get("Ws_up"), wts.get("Ws_gate"), wts.get("Ws_down")
+        if up is None or gate is None or down is None:
+            raise ValueError("the block needs Ws_up, Ws_gate and Ws_down")
+        if getattr(up, "ndim", 0) != 2 or getattr(x, "ndim", 0) != 2:
             raise ValueError("x must be [T, H] and Ws_up [D, H]")
-        (T, H), D = x.shape, wts["Ws_up"].shape[0]
-        _is_tensor(x, "x", (T, H), ("bfloat16",), device)
-        for n, shape in zip(names, ((D, H), (D, H), (H, D))):
-            _is_tensor(wts[n], n, shape, ("bfloat16",), device)
-        return T, H, D
+        (T, H), D, dev = x.shape, up.shape[0], self.device
+        _is_tensor(x, "x", (T, H), _BF16, dev)
+        _is_tensor(up, "Ws_up", (D, H), _BF16, dev)
+        _is_tensor(gate, "Ws_gate", (D, H), _BF16, dev)
+        _is_tensor(down, "Ws_down", (H, D), _BF16, dev)
+        return T, H, D, moe_shared_w(up.data_ptr(), gate.data_ptr(), down.data_ptr())
 
-    def _ffn_workspace(self, workspace, sizes, backward, device, stream):
+    def _ffn_workspace(self, workspace, need, stream):
         """The caller's workspace, or one for this call alone (allocated in the order of the
         call's stream, so that its memory is reused only behind the call)."""
         import torch
-        need = lib.moe_ffn_workspace_bytes(*sizes, backward)
-        if need < 0:
-            raise ValueError(f"the block takes multiples of 8 for its hidden and inner size, got {sizes[1]} and {sizes[2]}")
-        if workspace is None:
-            with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}")
-        elif workspace.numel() < need:
-            raise ValueError(f"the workspace needs {need} bytes, got {workspace.numel()}")
-        else:
-            _is_tensor(workspace, "workspace", workspace.shape, ("uint8",), device)
-        return workspace
+        if workspace is not None:
+            _is_tensor(workspace, "workspace", getattr(workspace, "shape", None), _U8, self.device)
+            if workspace.numel() < need:
+                raise ValueError(f"the workspace needs {need} bytes, got {workspace.numel()}")
+            return workspace
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", self.device))
+        with torch.cuda.stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", self.device))
 
     @staticmethod
     def ffn_workspace_bytes(T, hidden, inter, backward=False):
         """Bytes of the workspace of ffn_forward or ffn_backward (a uint8 tensor)."""
         n = lib.moe_ffn_workspace_bytes(T, hidden, inter, 1 if backward else 0)
         if n < 0:
-            raise ValueError(f"the block takes multiples of 8 for its hidden and inner size, got {hidden} and {inter}")
+            raise ValueError("the block's hidden and inner sizes are multiples of 8 up to 2^20, its tokens at most "
+                             f"2^24: got {hidden}, {inter} and {T}")
         return n
 
     def ffn_forward(self, x, wts, out, u=None, g=None, workspace=None, stream=None):
         """moe_ffn_forward: out = W_down (SiLU(W_up x) * (W_gate x)) with wts["Ws_up"] and
         wts["Ws_gate"] [D, H] and wts["Ws_down"] [H, D]; x [T, H] bf16, out [T, H] bf16 or fp32.
         u and g ([T, D] bf16, both or neither) receive the pre-activations for ffn_backward."""
-        dev = self.query(13)
-        T, H, D = self._ffn_sizes(x, wts, dev)
-        _is_tensor(out, "out", (T, H), ("bfloat16", "float32"), dev)
-        if (u is None) != (g is None):
-            raise ValueError("u and g go together")
-        for t, n in ((u, "u"), (g, "g")):
-            if t is not None:
-                _is_tensor(t, n, (T, D), ("bfloat16",), dev)
-        ws = self._ffn_workspace(workspace, (T, H, D), 0, dev, stream)
-        sh = self._shared(wts)
-        check(lib.moe_ffn_forward(self.h, _ptr(x), T, H, D, sh[0], _ptr(out), 1 if out.element_size() == 2 else 0,
-                                  _ptr(u), _ptr(g), _ptr(ws), ws.numel(), _stream(stream, dev)), "moe_ffn_forward")
+        T, H, D, w = self._ffn_call(x, wts)
+        _is_tensor(out, "out", (T, H), _BF16_F32, self.device)
+        if u is not None or g is not None:
+            if u is None or g is None:
+                raise ValueError("u and g go together")
+            _is_tensor(u, "u", (T, D), _BF16, self.device)
+            _is_tensor(g, "g", (T, D), _BF16, self.device)
+        ws = self._ffn_workspace(workspace, self.ffn_workspace_bytes(T, H, D), stream)
+        check(lib.moe_ffn_forward(self.h, x.data_ptr(), T, H, D, w, out.data_ptr(), 1 if out.element_size() == 2 else 0,
+                                  _addr(u), _addr(g), ws.data_ptr(), ws.numel(), _raw_stream(stream, self.device)),
+              "moe_ffn_forward")
         return out
 
     def ffn_backward(self, dout, x, u, g, wts, grads, accumulate=False, workspace=None, stream=None):
         """moe_ffn_backward: fills grads["x"] ([T, H] bf16) and grads["Ws_up"], grads["Ws_gate"],
         grads["Ws_down"] (shaped as the weights, all bf16 or all fp32; with accumulate, fp32 and
         added to). A gradient that grads lacks, or has as None, is not computed."""
-        dev = self.query(13)
-        T, H, D = self._ffn_sizes(x, wts, dev)
-        _is_tensor(dout, "dout", (T, H), ("bfloat16",), dev)
-        for t, n in ((u, "u"), (g, "g")):
-            _is_tensor(t, n, (T, D), ("bfloat16",), dev)
-        unknown = set(grads) - {"x", "Ws_up", "Ws_gate", "Ws_down"}
-        if unknown:
-            raise ValueError(f"no gradient named {sorted(unknown)}")
-        if grads.get("x") is not None:
-            _is_tensor(grads["x"], "grads['x']", (T, H), ("bfloat16",), dev)
-        dw = {n: grads.get(n) for n in ("Ws_up", "Ws_gate", "Ws_down")}
-        kinds = {str(t.dtype).split(".")[-1] for t in dw.values() if t is not None}
-        for n, t in dw.items():
+        T, H, D, w = self._ffn_call(x, wts)
+        dev = self.device
+        _is_tensor(dout, "dout", (T, H), _BF16, dev)
+        _is_tensor(u, "u", (T, D), _BF16, dev)
+        _is_tensor(g, "g", (T, D), _BF16, dev)
+        if not grads.keys() <= {"x", "Ws_up", "Ws_gate", "Ws_down"}:
+            raise ValueError(f"gradients are named x, Ws_up, Ws_gate and Ws_down, got {sorted(grads)}")
+        dx = grads.get("x")
+        if dx is not None:
+            _is_tensor(dx, "grads['x']", (T, H), _BF16, dev)
+        first, addr = None, []
+        for n in ("Ws_up", "Ws_gate", "Ws_down"):
+            t = grads.get(n)
             if t is not None:
-                _is_tensor(t, f"grads[{n!r}]", wts[n].shape, ("float32",) if accumulate else ("bfloat16", "float32"), dev)
-        if len(kinds) > 1:
-            raise TypeError("the weight gradients must all be bfloat16 or all float32")
-        flags = (MOE_FFN_GRAD_F32 if kinds == {"float32"} else 0) | (MOE_FFN_GRAD_ADD if accumulate and kinds else 0)
-        ws = self._ffn_workspace(workspace, (T, H, D), 1, dev, stream)
-        sh = self._shared(wts)
-        gr = moe_ffn_grads(*(None if t is None else t.data_ptr() for t in dw.values()))
-        check(lib.moe_ffn_backward(self.h, _ptr(dout), _ptr(x), _ptr(u), _ptr(g), T, H, D, sh[0],
-                                   _ptr(grads.get("x")), ctypes.byref(gr), flags, _ptr(ws), ws.numel(),
-                                   _stream(stream, dev)), "moe_ffn_backward")
+                _is_tensor(t, f"grads[{n!r}]", wts[n].shape, _F32 if accumulate else _BF16_F32, dev)
+                first = t if first is None else first
+                if t.dtype != first.dtype:
+                    raise TypeError("the weight gradients must all be bfloat16 or all float32")
+            addr.append(_addr(t))
+        flags = 0 if first is None or first.element_size() == 2 else MOE_FFN_GRAD_F32 | (MOE_FFN_GRAD_ADD if accumulate else 0)
+        ws = self._ffn_workspace(workspace, self.ffn_workspace_bytes(T, H, D, True), stream)
+        check(lib.moe_ffn_backward(self.h, dout.data_ptr(), x.data_ptr(), u.data_ptr(), g.data_ptr(), T, H, D, w,
+                                   _addr(dx), moe_ffn_grads(*addr), flags, ws.data_ptr(), ws.numel(),
+                                   _raw_stream(stream, dev)), "moe_ffn_backward")
         return grads
 
     # ---- MXFP8 experts ----
