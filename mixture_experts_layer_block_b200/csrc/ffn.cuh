@@ -41,8 +41,7 @@ struct alignas(64) FfnProblem {
 struct FfnParams {
   FfnProblem p[kFfnMaxProblems];
   CUtensorMap out2, out3;  // up: u, g (save); dh: dg, h
-  const uint16_t* u;       // dh: saved pre-activations [M][N]
-  const uint16_t* g;
+  CUtensorMap in_u, in_g;  // dh: the saved pre-activations [M][N], boxes of {32 columns, 128 rows}
   int32_t nprob, units;
   int32_t save;            // up: also store u and g
   DeviceMeta* meta;

@@ -149,7 +149,7 @@ int operand(moe_handle* h, CUtensorMap* m, const void* p, int64_t inner, int64_t
   return encode_map(h, m, p, inner, outer, (uint64_t)inner * 2, kBK, rows);
 }
 
-// A result of 16-bit (64-byte chunks) or 32-bit elements (128-byte chunks).
+// A result (or u, g on their way in) by 32-column chunks: 16-bit (64 bytes a row) or 32-bit elements (128 bytes).
 int result(moe_handle* h, CUtensorMap* m, void* p, int64_t cols, int64_t rows, bool f32, int64_t ld) {
   return encode_map(h, m, p, cols, rows, (uint64_t)ld * (f32 ? 4 : 2), 32, 128,
                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -317,8 +317,8 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   P.nprob = 1;
   fill_problem(P.p[0], b.dh, 1, false, true, 0);
   P.units = units_of(b.dh);
-  P.u = static_cast<const uint16_t*>(u);
-  P.g = static_cast<const uint16_t*>(g);
+  if ((rc = result(h, &P.in_u, const_cast<void*>(u), D, T, false, D))) return rc;
+  if ((rc = result(h, &P.in_g, const_cast<void*>(g), D, T, false, D))) return rc;
   if ((rc = operand(h, &P.p[0].a[0], dout, H, T, 128))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->down, D, H, 64))) return rc;
   if ((rc = set_result(h, P.p[0], b.dh, du, 0, ws + b.dh_parts))) return rc;
@@ -329,8 +329,8 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
     FfnReduce r = reduce_of(b.dh, ws + b.dh_parts, du, 0);
     r.out2 = static_cast<uint16_t*>(dg);
     r.out3 = static_cast<uint16_t*>(hb);
-    r.u = P.u;
-    r.g = P.g;
+    r.u = static_cast<const uint16_t*>(u);
+    r.g = static_cast<const uint16_t*>(g);
     if ((rc = cuda_rc(launch_ffn_reduce(r, kFfnDSwiglu, h->num_sms, st)))) return rc;
   }
   // the four gradients in one launch

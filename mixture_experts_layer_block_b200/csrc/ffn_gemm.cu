@@ -21,7 +21,9 @@
 // order, so that results do not depend on timing.
 //
 // Warp roles per CTA: warps 0 and 6 TMA producers (A and B), warp 1 MMA issuer (CTA 0), warps 2-5
-// epilogue.
+// epilogue, warp 7 (dh only) the epilogue's loads of u and g and its stores: with 16-byte loads by
+// the epilogue's own threads, each of another row, a tile's epilogue took 25,000 clocks and slowed
+// the products beside it by a third.
 #include <algorithm>
 
 #include "ffn.cuh"
@@ -31,7 +33,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kFThreads = 224;
+constexpr int kFThreads = 256;
 constexpr int kFMaxStages = 8;
 constexpr int kFABytes = 128 * kBK * 2;  // 16 KB of A per CTA and stage
 constexpr int kFBoxBytes = 64 * 64 * 2;  // an MN-major box of 64 x 64
@@ -126,7 +128,9 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   uint64_t* empty = full + kFMaxStages;
   uint64_t* acc_full = empty + kFMaxStages;
   uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* ug_full = acc_empty + 2;   // dh: u and g of a chunk are in its buffer
+  uint64_t* ready = ug_full + 2;       // dh: du, dg and h of a chunk are in its buffer
+  uint64_t* drain = ready + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_go = reinterpret_cast<volatile int*>(s_tmem + 2);           // [2]
@@ -151,6 +155,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 8);  // 4 epilogue warps x 2 CTAs
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ug_full[i], 1);
+      mbar_init(&ready[i], 128);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -258,6 +266,62 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       }
     }
     __syncwarp();
+  } else if (warp == 7) {
+    // ------------- dh: u and g into the staging buffers, du, dg and h out of them -------------
+    if (kEpi == kFfnDSwiglu && P.p[0].splits == 1 && elect_one()) {
+      const FfnProblem& p = P.p[0];
+      const int nchunk = (p.bn + kFChunk - 1) / kFChunk;
+      struct Cursor {
+        int id, cc, col, row;
+      } in{pair, 0, 0, 0}, out{pair, 0, 0, 0};
+      auto place = [&](Cursor& c) {
+        const Unit t = find_unit_ffn(P, c.id);
+        c.col = t.n * p.bn;
+        c.row = t.m * kFfnTileM + (int)rank * 128;
+      };
+      auto next = [&](Cursor& c) {
+        if (++c.cc == nchunk) {
+          c.cc = 0;
+          c.id += npairs;
+          if (c.id < P.units) place(c);
+        }
+      };
+      place(in);
+      place(out);
+      uint32_t loads = 0;
+      auto load = [&]() {  // the next chunk's u and g into buffer loads % 2, which is free
+        const uint32_t b = loads & 1;
+        const uint32_t dst = smem_u32(staging) + b * 24576;
+        const int col = in.col + chunk_col(in.cc, p.bn);
+        mbar_arrive_expect_tx(&ug_full[b], 16384);
+        tma_load_2d(dst, &P.in_u, &ug_full[b], col, in.row);
+        tma_load_2d(dst + 8192, &P.in_g, &ug_full[b], col, in.row);
+        ++loads;
+        next(in);
+      };
+      for (int i = 0; i < 2 && in.id < P.units; ++i) load();
+      for (uint32_t n = 0; out.id < P.units; ++n) {
+        const uint32_t b = n & 1;
+        if (!wait_bar(&ready[b], (n >> 1) & 1, meta, s_abort, limit, kSiteEpiTask)) break;
+        const uint32_t src = smem_u32(staging) + b * 24576;
+        const int col = out.col + chunk_col(out.cc, p.bn);
+        if (out.row < p.nrows && col < p.ncols) {
+          tma_store_2d(&p.out, src, col, out.row);
+          tma_store_2d(&P.out2, src + 8192, col, out.row);
+          tma_store_2d(&P.out3, src + 16384, col, out.row);
+        }
+        bulk_commit_group();
+        next(out);
+        if (in.id < P.units) {
+          bulk_wait_group_read<0>();
+          load();
+        }
+      }
+      bulk_wait_group<0>();
+      for (uint32_t b = 0; b < 2; ++b)  // after an abort, loads that nobody waited for
+        if (loads > b) wait_bar_drain(&ug_full[b], (((loads - 1 - b) >> 1)) & 1, meta, limit);
+    }
+    __syncwarp();
   } else {
     // ----------------------------------- epilogue -----------------------------------
     // Each thread owns one row of the CTA's 128. A step takes 32 columns: bf16 results are staged
@@ -265,7 +329,14 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     const int q = warp & 3;
     const int row = q * 32 + lane;
     const bool leader = (warp == 2 && lane == 0);
-    uint32_t acc = 0, acc_phase = 0, sb = 0;
+    uint32_t acc = 0, acc_phase = 0, sb = 0, ug_phase = 0;
+    auto get_bf16 = [&](const uint8_t* buf, uint32_t (&w)[16]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4*>(buf + row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
+        w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
+      }
+    };
     auto put_bf16 = [&](uint8_t* buf, const uint32_t (&w)[16]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -283,23 +354,6 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       const Unit t = find_unit_ffn(P, id);
       const FfnProblem& p = P.p[t.prob];
       const int m0 = t.m * kFfnTileM + (int)rank * 128;
-      // dh: a chunk of this row's u and g, requested a chunk ahead (the first before the wait)
-      const bool mine = kEpi == kFfnDSwiglu && m0 + row < p.nrows;
-      uint4 un[4], gn[4];
-      auto fetch = [&](int cc) {
-        const int col = t.n * p.bn + chunk_col(cc, p.bn);
-        const size_t base = (size_t)(mine ? m0 + row : 0) * p.ncols + col;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // ncols is a multiple of 8: a 16-byte vector is inside or outside as a whole
-          const bool in = mine && col + 8 * j < p.ncols;
-          un[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.u + base + 8 * j)) : make_uint4(0, 0, 0, 0);
-          gn[j] = in ? __ldg(reinterpret_cast<const uint4*>(P.g + base + 8 * j)) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      if constexpr (kEpi == kFfnDSwiglu) {
-        if (p.splits == 1) fetch(0);
-      }
       // one thread waits for the accumulator and tells the other 127, so that the warps always
       // leave the loop together
       if (leader) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
@@ -396,19 +450,18 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           sb ^= 1;
         }
       } else if constexpr (kEpi == kFfnDSwiglu) {
+        // warp 7 brings u and g of a chunk into its buffer; this thread replaces its row of them by
+        // du and dg, adds h, and hands the buffer back for warp 7 to store. A wait that gives up
+        // only spoils results: the loop ends at the next tile.
         const int nchunk = (p.bn + kFChunk - 1) / kFChunk;
 #pragma unroll 1
         for (int cc = 0; cc < nchunk; ++cc) {
-          const int c0 = chunk_col(cc, p.bn);
-          uint32_t v[32], du[16], dg[16], hh[16];
-          tmem_ld_32x32b_x32(tacc + c0, v);
-          uint32_t uw[16], gw[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uw[4 * j] = un[j].x; uw[4 * j + 1] = un[j].y; uw[4 * j + 2] = un[j].z; uw[4 * j + 3] = un[j].w;
-            gw[4 * j] = gn[j].x; gw[4 * j + 1] = gn[j].y; gw[4 * j + 2] = gn[j].z; gw[4 * j + 3] = gn[j].w;
-          }
-          if (cc + 1 < nchunk) fetch(cc + 1);
+          uint32_t v[32], uw[16], gw[16], hh[16];
+          uint8_t* buf = staging + sb * 24576;
+          wait_bar_fast(&ug_full[sb], ug_phase, meta, s_abort, limit, kSiteEpiTask);
+          tmem_ld_32x32b_x32(tacc + chunk_col(cc, p.bn), v);
+          get_bf16(buf, uw);
+          get_bf16(buf + 8192, gw);
           tmem_ld_wait();
           if (cc == nchunk - 1) release();
 #pragma unroll
@@ -417,28 +470,17 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
             dswiglu(__uint_as_float(v[2 * j]), __uint_as_float(uw[j] << 16), __uint_as_float(gw[j] << 16), a0, b0, c0);
             dswiglu(__uint_as_float(v[2 * j + 1]), __uint_as_float(uw[j] & 0xffff0000u),
                     __uint_as_float(gw[j] & 0xffff0000u), a1, b1, c1);
-            du[j] = pack_bf16x2(a0, a1);
-            dg[j] = pack_bf16x2(b0, b1);
+            uw[j] = pack_bf16x2(a0, a1);
+            gw[j] = pack_bf16x2(b0, b1);
             hh[j] = pack_bf16x2(c0, c1);
           }
-          uint8_t* buf = staging + sb * 24576;
-          if (leader) bulk_wait_group_read<1>();
-          named_bar_sync(1, 128);
-          put_bf16(buf, du);
-          put_bf16(buf + 8192, dg);
+          put_bf16(buf, uw);
+          put_bf16(buf + 8192, gw);
           put_bf16(buf + 16384, hh);
           fence_proxy_async_shared();
-          named_bar_sync(1, 128);
-          if (leader) {
-            const int col = t.n * p.bn + c0;
-            if (rows_in && col < p.ncols) {
-              tma_store_2d(&p.out, smem_u32(buf), col, m0);
-              tma_store_2d(&P.out2, smem_u32(buf) + 8192, col, m0);
-              tma_store_2d(&P.out3, smem_u32(buf) + 16384, col, m0);
-            }
-            bulk_commit_group();
-          }
+          mbar_arrive(&ready[sb]);
           sb ^= 1;
+          if (sb == 0) ug_phase ^= 1;
         }
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
