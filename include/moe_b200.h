@@ -247,6 +247,84 @@ MOE_API int moe_forward_mxfp8(moe_handle *h, const void *x, int32_t T, const voi
                               const float *router_bias, const moe_mxfp8_experts *w, int32_t top_k,
                               void *out, void *stream);
 
+/* ---- 4-bit experts for decode batches --------------------------------------------------------
+ * A matrix [R][K] (K a multiple of 8) in 4 bits: w[r][c] = s[r][c/G] * (q[r][c] - z[r][c/G]) with
+ * codes q and zero points z in 0..15 (z = 8 where a matrix has none), bf16 scales s, and groups
+ * of G = 32, 64 or 128 consecutive columns (the last one may be shorter). The library keeps it
+ * in a layout of its own, two device buffers owned by the caller, 16-byte aligned:
+ *   codes   moe_int4_code_bytes(R, K) bytes: blocks of 16 rows x 64 columns, 512 bytes each, at
+ *           (r / 16) * ceil(K / 64) + c / 64; rows and columns past the edge are padding. In a
+ *           block, the 16 bytes at (4 i + j) * 16 (i < 8, j < 4) hold the columns 8 j .. 8 j + 7 and
+ *           32 + 8 j .. 32 + 8 j + 7 of rows i and i + 8: 32-bit word 2 h + m (h, m < 2) holds, from
+ *           bit 0 up in steps of 4, with k = 32 h + 8 j + 4 m: (i, k), (i + 8, k), (i, k + 2),
+ *           (i + 8, k + 2), (i, k + 1), (i + 8, k + 1), (i, k + 3), (i + 8, k + 3).
+ *   scales  moe_int4_scale_bytes(R, K, G, zeros) bytes: per 16 rows and group, at
+ *           (r / 16) * ceil(K / G) + g, 16 entries in the row order 0, 8, 1, 9, ...: the bf16 scale
+ *           or, with zero points, 32 bits: the scale (low half) and bf16(128 + z) (high half).
+ * moe_quantize_int4 and moe_pack_int4 write it. Products are exact in fp32 up to the order and
+ * rounding of fp32 sums; the order is fixed, so equal inputs give equal bits. Meant for few
+ * tokens, where the weights' bytes are the cost (prefill: moe_forward with bf16 weights). */
+typedef struct moe_int4_mat {
+    const void *codes;
+    const void *scales;
+} moe_int4_mat;
+
+/* The experts of moe_experts_int4 and moe_forward_int4, stacked as in moe_forward_mxfp8: up and
+ * gate [E*D][H], down [E*H][D]; the shared expert's (ignored when D_shared == 0) [D_shared][H],
+ * [D_shared][H] and [H][D_shared]. All with the same group size, all with zero points or none. */
+typedef struct moe_int4_experts {
+    moe_int4_mat up, gate, down;
+    moe_int4_mat shared_up, shared_gate, shared_down;
+    int32_t group;
+    int32_t zeros;
+} moe_int4_experts;
+
+/* Bytes of a matrix's two buffers; -1 unless rows >= 1, cols is a multiple of 8 (8..2^24) and group
+ * is 32, 64 or 128. */
+MOE_API int64_t moe_int4_code_bytes(int64_t rows, int64_t cols);
+MOE_API int64_t moe_int4_scale_bytes(int64_t rows, int64_t cols, int32_t group, int32_t zeros);
+
+/* Quantise the device bf16 matrix src [rows][cols] (finite, magnitudes below 1e38), group by group
+ * in fp32, to nearest even. Without zero points s = bf16(max|v| / 7), q = v / s + 8; with them
+ * s = bf16((max - min) / 15), z = -min / s, q = v / s + z, where max and min also count 0; z and q
+ * are clamped to 0..15. A group whose scale is 0 has q = z = 8. Any handle works. */
+MOE_API int moe_quantize_int4(moe_handle *h, const void *src, int64_t rows, int64_t cols, int32_t group,
+                              int32_t zeros, void *codes, void *scales, void *stream);
+
+/* Lay out a matrix that is already quantised, as checkpoints hold it: q device uint8
+ * [rows][cols / 2], two codes a byte (the even column in the low half); s device bf16
+ * [rows][ceil(cols / group)]; z device uint8 of the same shape (0..15), or NULL for none. Any handle
+ * works. Both calls: MOE_ERR_INVALID_ARG for a size or group that moe_int4_scale_bytes refuses,
+ * MOE_ERR_MISALIGNED for a pointer off a 16-byte boundary. */
+MOE_API int moe_pack_int4(moe_handle *h, const uint8_t *q, const void *s, const uint8_t *z, int64_t rows,
+                          int64_t cols, int32_t group, void *codes, void *scales, void *stream);
+
+/* out[t] = W x[t]: x device bf16 [T][cols], out device [T][rows], bf16 (out_bf16 = 1, rounded once)
+ * or fp32 (on its own type's boundary: rows may be any number). Any handle works. Any T (0..2^24), but every 16 tokens are a launch that reads the
+ * weights again. rows up to 2^31 - 1. No scratch memory: calls on different streams may overlap. */
+MOE_API int moe_matvec_int4(moe_handle *h, const void *x, int64_t T, const moe_int4_mat *w, int64_t rows,
+                            int64_t cols, int32_t group, int32_t zeros, void *out, int32_t out_bf16,
+                            void *stream);
+
+/* The layer behind its gating, with 4-bit experts, for T <= 16 tokens (more: MOE_ERR_UNSUPPORTED):
+ *     out[t] = W_shared(x[t]) + sum_j topk_w[t][j] * W_down^e SwiGLU(W_up^e x[t], W_gate^e x[t])
+ * with e = topk_ids[t][j] (device int32 [T][top_k]; an id outside [0, E) contributes nothing, one
+ * that a token names twice counts twice; no capacity is applied), topk_w device fp32 [T][top_k].
+ * h is rounded to bf16 as in moe_forward; the router-weighted sums stay in fp32. x device bf16
+ * [T][H]; out device [T][H], bf16 or fp32, fully overwritten. Needs H and D multiples of 16 (else
+ * MOE_ERR_UNSUPPORTED). Uses the handle's workspace, as moe_forward does: the two must not overlap
+ * on one handle, and moe_debug_outputs has nothing to show afterwards. */
+MOE_API int moe_experts_int4(moe_handle *h, const void *x, int32_t T, const int32_t *topk_ids,
+                             const float *topk_w, int32_t top_k, const moe_int4_experts *w, void *out,
+                             int32_t out_bf16, void *stream);
+
+/* moe_forward with 4-bit experts, for T <= 16 tokens: router projection and gating as the separate
+ * kernels of moe_forward (MOE_FLAG_UNFUSED_SMALL), capacity as there, then moe_experts_int4. out
+ * device fp32 [T][H], or bf16 with MOE_FLAG_OUT_BF16. */
+MOE_API int moe_forward_int4(moe_handle *h, const void *x, int32_t T, const void *w_router,
+                             const float *router_bias, const moe_int4_experts *w, int32_t top_k, void *out,
+                             void *stream);
+
 /* ---- the gated feed-forward block, forward and backward -------------------------------------
  * The layer equation's W_shared(x) term on its own, for any token count and any sizes: a dense
  * layer's FFN, or the shared expert's training step.

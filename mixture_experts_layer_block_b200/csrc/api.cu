@@ -99,6 +99,30 @@ int router_bn(int E, int T, int num_sms) {
 
 }  // namespace
 
+namespace moe {
+
+int forward_capacity(const moe_handle* h, int T, int k) { return capacity_of(h->cfg, T, k); }
+
+// The router projection and the gating of a forward, into the workspace's topk_ids and topk_w.
+int run_router_and_gate(moe_handle* h, const void* x, int32_t T, const void* w_router, const float* router_bias,
+                        int32_t top_k, cudaStream_t st) {
+  const int E = h->cfg.num_experts, H = h->cfg.hidden, bn = router_bn(E, T, h->num_sms);
+  const Workspace& w = h->ws;
+  CUtensorMap xm, wm;
+  int rc;
+  if ((rc = encode_map(h, &xm, x, H, T, (uint64_t)H * 2, kBK, kBM))) return rc;
+  if ((rc = cached_map(h, &wm, w_router, H, E, (uint64_t)H * 2, kBK, bn))) return rc;
+  int splits = router_splits(T, E, H, bn, h->num_sms);
+  while (splits > 1 && (int64_t)splits * T > h->parts_rows) splits /= 2;
+  float* parts = splits > 1 ? w.logit_parts : w.logits;
+  if ((rc = check_cuda(launch_router(xm, wm, router_bias, parts, T, E, H, bn, splits, w.meta, h->timeout_ns, st))))
+    return rc;
+  return check_cuda(launch_gate(parts, splits, splits > 1 ? w.logits : nullptr, w.topk_ids, w.topk_w, w,
+                                make_shape(h, T, top_k), false, false, 0, st));
+}
+
+}  // namespace moe
+
 extern "C" {
 
 const char* moe_status_string(int code) {

@@ -27,7 +27,7 @@ struct alignas(64) FfnProblem {
                            // b[r] is what CTA r of the pair stages (W_up rows | W_gate rows)
   CUtensorMap out;         // bf16 or fp32 [M][N] (fp32 partials [splits * mpad][N] when splits > 1)
   int32_t mt, nt;          // tiles along M and N
-  int32_t bn;              // columns per tile, a multiple of 16 (u | g: of 32) in 128..256
+  int32_t bn;              // columns per tile, a multiple of 16 in 128..256
   int32_t nrows, ncols;    // M, N (what lies past them is not stored)
   int32_t nkb, nseg;       // 64-wide K blocks per segment, segments
   int32_t a_mn, b_mn;      // 1: MN-major

@@ -4,6 +4,7 @@
 
 #include "ffn.cuh"
 #include "handle.h"
+#include "matvec.cuh"
 
 using namespace moe;
 
@@ -17,6 +18,7 @@ struct Product {
   int64_t M, N;  // of the output (dual: of one of the two halves)
   int nkb;       // 64-wide K blocks in all
   bool dual;     // u and g side by side
+  bool b_mn;     // B has n contiguous
   // the plan
   int bn, mt, nt, splits;
   int64_t part_ld, part_bytes;  // fp32 partials: row stride in elements, bytes over all splits
@@ -30,7 +32,7 @@ void shape_product(Product& p, int bn, int splits) {
   const int cols = p.dual ? bn / 2 : bn;
   p.nt = (int)((p.N + cols - 1) / cols);
   p.splits = splits;
-  // a stored chunk is 32 columns wide and may start at any multiple of 16 below N: g's part starts
+  // a stored chunk is 32 columns wide and may start at any multiple of 8 below N: g's part starts
   // past the end of u's last chunk
   p.part_ld = p.dual ? 2 * (round_up(p.N, 16) + 32) : p.N;
   p.part_bytes = splits > 1 ? (int64_t)splits * p.mt * kFfnTileM * p.part_ld * 4 : 0;
@@ -42,17 +44,21 @@ void shape_product(Product& p, int bn, int splits) {
 //  - a unit's fill and drain that nothing overlaps takes about 2500;
 //  - with more than one unit a pair, the last round is as long as a full one;
 //  - partial sums cost a second launch (about 6000) and their bytes, written and read once.
-// Narrow tiles fill the last round better and wide ones feed the tensor cores better.
+// Narrow tiles fill the last round better and wide ones feed the tensor cores better. Where B has n
+// contiguous, both CTAs' boxes have to start on a 128-byte line, so the width is 128 or 256: a
+// box of 64 columns across two lines costs two requests a row (dh at 4096 tokens, hidden 7168, inner
+// 2048: 650 clocks a K block at 240 columns, 530 at 256).
 void plan(Product* p, int n) {
   int best_bn = 256, best_L = 1 << 30;
   double best = 1e30;
-  bool dual = false;
+  bool dual = false, b_mn = false;
   int most = 1;
   for (int i = 0; i < n; ++i) {
     dual = dual || p[i].dual;
+    b_mn = b_mn || p[i].b_mn;
     most = std::max(most, p[i].nkb);
   }
-  for (int bn = 128; bn <= 256; bn += dual ? 32 : 16) {
+  for (int bn = 128; bn <= 256; bn += b_mn ? 128 : 16) {
     for (int L = most; L >= 4 || L == most; L = L / 2) {
       double total = 0, longest = 0, parts = 0;
       int64_t units = 0;
@@ -100,8 +106,14 @@ struct ForwardPlan {
 
 ForwardPlan plan_forward(int64_t T, int64_t H, int64_t D) {
   ForwardPlan f{};
-  f.up = Product{T, D, blocks_of(H), true};
-  f.down = Product{T, H, blocks_of(D), false};
+  if (T <= kMvTokens) {  // only h: the small-batch products keep their partial sums on the chip
+    Layout l;
+    f.h = l.take(T * D * 2);
+    f.bytes = l.at;
+    return f;
+  }
+  f.up = Product{T, D, blocks_of(H), true, false};
+  f.down = Product{T, H, blocks_of(D), false, false};
   plan(&f.up, 1);
   plan(&f.down, 1);
   Layout l;
@@ -120,12 +132,12 @@ struct BackwardPlan {
 // Planned as if every gradient is asked for: a call that leaves some out runs the others' plan.
 BackwardPlan plan_backward(int64_t T, int64_t H, int64_t D) {
   BackwardPlan b{};
-  b.dh = Product{T, D, blocks_of(H), false};
+  b.dh = Product{T, D, blocks_of(H), false, true};
   plan(&b.dh, 1);
-  b.rest[0] = Product{T, H, 2 * blocks_of(D), false};
-  b.rest[1] = Product{D, H, blocks_of(T), false};
+  b.rest[0] = Product{T, H, 2 * blocks_of(D), false, true};
+  b.rest[1] = Product{D, H, blocks_of(T), false, true};
   b.rest[2] = b.rest[1];
-  b.rest[3] = Product{H, D, blocks_of(T), false};
+  b.rest[3] = Product{H, D, blocks_of(T), false, true};
   plan(b.rest, 4);
   Layout l;
   b.du = l.take(T * D * 2);
@@ -156,7 +168,7 @@ int result(moe_handle* h, CUtensorMap* m, void* p, int64_t cols, int64_t rows, b
                     f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-void fill_problem(FfnProblem& f, const Product& p, int nseg, bool a_mn, bool b_mn, int unit0) {
+void fill_problem(FfnProblem& f, const Product& p, int nseg, bool a_mn, int unit0) {
   f.mt = p.mt;
   f.nt = p.nt;
   f.bn = p.bn;
@@ -165,7 +177,7 @@ void fill_problem(FfnProblem& f, const Product& p, int nseg, bool a_mn, bool b_m
   f.nseg = nseg;
   f.nkb = p.nkb / nseg;
   f.a_mn = a_mn;
-  f.b_mn = b_mn;
+  f.b_mn = p.b_mn;
   f.b_by_rank = p.dual;
   f.splits = p.splits;
   f.mpad = p.mt * kFfnTileM;
@@ -241,12 +253,35 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   char* ws = static_cast<char*>(workspace);
   void* hb = ws + f.h;
 
+  if (T <= kMvTokens) {
+    // at most 16 tokens: the weights' bytes are the cost, and the tensor-core tiles would be empty
+    MvArgs a{};
+    a.m = MvMatrix{{w->up, w->gate}, {nullptr, nullptr}, (int32_t)D, (int32_t)H};
+    a.x = static_cast<const uint16_t*>(x);
+    a.ldx = H;
+    a.T = (int32_t)T;
+    a.out = hb;
+    a.ldo = D;
+    a.out_bf16 = 1;
+    a.u = static_cast<uint16_t*>(u);
+    a.g = static_cast<uint16_t*>(g);
+    if ((rc = cuda_rc(launch_mv_bf16(a, true, h->num_sms, st)))) return rc;
+    a.m = MvMatrix{{w->down, nullptr}, {nullptr, nullptr}, (int32_t)H, (int32_t)D};
+    a.x = static_cast<const uint16_t*>(hb);
+    a.ldx = D;
+    a.early = 1;
+    a.out = out;
+    a.ldo = H;
+    a.out_bf16 = out_bf16 != 0;
+    a.u = a.g = nullptr;
+    return cuda_rc(launch_mv_bf16(a, false, h->num_sms, st));
+  }
   FfnParams P{};
   P.meta = h->ffn_meta;
   P.timeout_ns = h->timeout_ns;
   P.nprob = 1;
   // u and g side by side, h from the epilogue
-  fill_problem(P.p[0], f.up, 1, false, false, 0);
+  fill_problem(P.p[0], f.up, 1, false, 0);
   P.units = units_of(f.up);
   P.save = u != nullptr;
   if ((rc = operand(h, &P.p[0].a[0], x, H, T, 128))) return rc;
@@ -266,7 +301,7 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   }
   // out = h W_down^T
   const int kind = out_bf16 ? 0 : 1;
-  fill_problem(P.p[0], f.down, 1, false, false, 0);
+  fill_problem(P.p[0], f.down, 1, false, 0);
   P.units = units_of(f.down);
   if ((rc = operand(h, &P.p[0].a[0], hb, D, T, 128))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->down, D, H, f.down.bn / 2))) return rc;
@@ -315,7 +350,7 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   P.timeout_ns = h->timeout_ns;
   // dh = dout W_down, and du, dg and h from the epilogue
   P.nprob = 1;
-  fill_problem(P.p[0], b.dh, 1, false, true, 0);
+  fill_problem(P.p[0], b.dh, 1, false, 0);
   P.units = units_of(b.dh);
   if ((rc = result(h, &P.in_u, const_cast<void*>(u), D, T, false, D))) return rc;
   if ((rc = result(h, &P.in_g, const_cast<void*>(g), D, T, false, D))) return rc;
@@ -348,7 +383,7 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   for (int i = 0; i < 4; ++i) {
     if (!want[i].out) continue;
     FfnProblem& f = P.p[n++];
-    fill_problem(f, b.rest[i], i == 0 ? 2 : 1, i != 0, true, units);
+    fill_problem(f, b.rest[i], i == 0 ? 2 : 1, i != 0, units);
     units += units_of(b.rest[i]);
     for (int s = 0; s < (i == 0 ? 2 : 1); ++s) {
       if ((rc = operand(h, &f.a[s], want[i].a[s], want[i].am, T, i == 0 ? 128 : 64))) return rc;

@@ -38,10 +38,15 @@ constexpr int kFMaxStages = 8;
 constexpr int kFABytes = 128 * kBK * 2;  // 16 KB of A per CTA and stage
 constexpr int kFBoxBytes = 64 * 64 * 2;  // an MN-major box of 64 x 64
 constexpr int kFChunk = 32;              // columns per epilogue step
-constexpr int kFBarBytes = 256;
+constexpr int kFBarBytes = 512;
 constexpr int kFSmem = 227 * 1024 - 1024;  // less the alignment slack
-// three results per tile (h, u, g or du, dg, h) are staged at once, twice
-__host__ __device__ constexpr int staging_bytes(int epi) { return epi == kFfnStore ? 32 * 1024 : 48 * 1024; }
+// Epilogue buffers: two chunks of one result (16 KB each, fp32), of three (h, u, g: 24 KB), or (dh)
+// two chunks of u and g (16 KB) and one of du, dg and h (24 KB).
+__host__ __device__ constexpr int staging_bytes(int epi) {
+  return (epi == kFfnStore ? 32 : (epi == kFfnSwiglu ? 48 : 56)) * 1024;
+}
+constexpr int kFInBytes = 16384;               // u and g of a chunk
+constexpr int kFOutOff = 2 * kFInBytes;        // du, dg and h of a chunk
 __host__ __device__ constexpr int ring_bytes(int epi) { return kFSmem - staging_bytes(epi) - kFBarBytes; }
 
 // B's bytes per CTA and stage: bn / 2 rows of 128 bytes, or whole 64-wide boxes
@@ -106,8 +111,8 @@ __device__ __forceinline__ Unit find_unit_ffn(const FfnParams& P, int id) {
   return t;
 }
 
-// First column of a tile's chunk `cc`. A width that is an odd multiple of 16 ends in a chunk that
-// overlaps the one before it by 16 columns: they are stored twice, with the same values.
+// First column of a tile's chunk `cc`. A width that is no multiple of 32 ends in a chunk that
+// overlaps the one before it: those columns are stored twice, with the same values.
 __device__ __forceinline__ int chunk_col(int cc, int width) { return min(cc * kFChunk, width - kFChunk); }
 
 __device__ __forceinline__ void split_range(const FfnProblem& p, int split, int& k0, int& k1) {
@@ -129,8 +134,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   uint64_t* acc_full = empty + kFMaxStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* ug_full = acc_empty + 2;   // dh: u and g of a chunk are in its buffer
-  uint64_t* ready = ug_full + 2;       // dh: du, dg and h of a chunk are in its buffer
-  uint64_t* drain = ready + 2;
+  uint64_t* ug_free = ug_full + 2;     // dh: every thread has read its row of them
+  uint64_t* ready = ug_free + 2;       // dh: du, dg and h of a chunk are in the out buffer
+  uint64_t* out_free = ready + 1;      // dh: they have been read
+  uint64_t* drain = out_free + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_go = reinterpret_cast<volatile int*>(s_tmem + 2);           // [2]
@@ -158,8 +165,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ug_full[i], 1);
-      mbar_init(&ready[i], 128);
+      mbar_init(&ug_free[i], 128);
     }
+    mbar_init(ready, 128);
+    mbar_init(out_free, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
     for (int i = 0; i < 4; ++i) s_nfill[i] = 0;
@@ -291,19 +300,22 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       uint32_t loads = 0;
       auto load = [&]() {  // the next chunk's u and g into buffer loads % 2, which is free
         const uint32_t b = loads & 1;
-        const uint32_t dst = smem_u32(staging) + b * 24576;
+        const uint32_t dst = smem_u32(staging) + b * kFInBytes;
         const int col = in.col + chunk_col(in.cc, p.bn);
-        mbar_arrive_expect_tx(&ug_full[b], 16384);
+        mbar_arrive_expect_tx(&ug_full[b], kFInBytes);
         tma_load_2d(dst, &P.in_u, &ug_full[b], col, in.row);
         tma_load_2d(dst + 8192, &P.in_g, &ug_full[b], col, in.row);
         ++loads;
         next(in);
       };
       for (int i = 0; i < 2 && in.id < P.units; ++i) load();
+      const uint32_t src = smem_u32(staging) + kFOutOff;
       for (uint32_t n = 0; out.id < P.units; ++n) {
-        const uint32_t b = n & 1;
-        if (!wait_bar(&ready[b], (n >> 1) & 1, meta, s_abort, limit, kSiteEpiTask)) break;
-        const uint32_t src = smem_u32(staging) + b * 24576;
+        if (in.id < P.units) {
+          if (!wait_bar_fast(&ug_free[n & 1], (n >> 1) & 1, meta, s_abort, limit, kSiteEpiTask)) break;
+          load();
+        }
+        if (!wait_bar_fast(ready, n & 1, meta, s_abort, limit, kSiteEpiTask)) break;
         const int col = out.col + chunk_col(out.cc, p.bn);
         if (out.row < p.nrows && col < p.ncols) {
           tma_store_2d(&p.out, src, col, out.row);
@@ -311,11 +323,9 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           tma_store_2d(&P.out3, src + 16384, col, out.row);
         }
         bulk_commit_group();
+        bulk_wait_group_read<0>();
+        mbar_arrive(out_free);
         next(out);
-        if (in.id < P.units) {
-          bulk_wait_group_read<0>();
-          load();
-        }
       }
       bulk_wait_group<0>();
       for (uint32_t b = 0; b < 2; ++b)  // after an abort, loads that nobody waited for
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     const int q = warp & 3;
     const int row = q * 32 + lane;
     const bool leader = (warp == 2 && lane == 0);
-    uint32_t acc = 0, acc_phase = 0, sb = 0, ug_phase = 0;
+    uint32_t acc = 0, acc_phase = 0, sb = 0, ug_phase = 0, out_phase = 0;
     auto get_bf16 = [&](const uint8_t* buf, uint32_t (&w)[16]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -385,7 +395,8 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           named_bar_sync(1, 128);
           if (p.out_kind == 2 && c0 < cc * kFChunk) {  // columns that the chunk before has added
 #pragma unroll
-            for (int j = 0; j < kFChunk / 2; ++j) v[j] = 0;
+            for (int j = 0; j < kFChunk; ++j)
+              if (c0 + j < cc * kFChunk) v[j] = 0;
           }
           if (p.out_kind == 0) {
             uint32_t pk[16];
@@ -450,18 +461,19 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           sb ^= 1;
         }
       } else if constexpr (kEpi == kFfnDSwiglu) {
-        // warp 7 brings u and g of a chunk into its buffer; this thread replaces its row of them by
-        // du and dg, adds h, and hands the buffer back for warp 7 to store. A wait that gives up
-        // only spoils results: the loop ends at the next tile.
+        // warp 7 brings u and g of a chunk, two chunks ahead, and stores du, dg and h from the out
+        // buffer. A wait that gives up only spoils results: the loop ends at the next tile.
         const int nchunk = (p.bn + kFChunk - 1) / kFChunk;
 #pragma unroll 1
         for (int cc = 0; cc < nchunk; ++cc) {
           uint32_t v[32], uw[16], gw[16], hh[16];
-          uint8_t* buf = staging + sb * 24576;
-          wait_bar_fast(&ug_full[sb], ug_phase, meta, s_abort, limit, kSiteEpiTask);
+          const uint8_t* inb = staging + sb * kFInBytes;
+          uint8_t* buf = staging + kFOutOff;
           tmem_ld_32x32b_x32(tacc + chunk_col(cc, p.bn), v);
-          get_bf16(buf, uw);
-          get_bf16(buf + 8192, gw);
+          wait_bar_fast(&ug_full[sb], ug_phase, meta, s_abort, limit, kSiteEpiTask);
+          get_bf16(inb, uw);
+          get_bf16(inb + 8192, gw);
+          mbar_arrive(&ug_free[sb]);
           tmem_ld_wait();
           if (cc == nchunk - 1) release();
 #pragma unroll
@@ -474,11 +486,13 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
             gw[j] = pack_bf16x2(b0, b1);
             hh[j] = pack_bf16x2(c0, c1);
           }
+          wait_bar_fast(out_free, out_phase ^ 1, meta, s_abort, limit, kSiteEpiTask);
           put_bf16(buf, uw);
           put_bf16(buf + 8192, gw);
           put_bf16(buf + 16384, hh);
           fence_proxy_async_shared();
-          mbar_arrive(&ready[sb]);
+          mbar_arrive(ready);
+          out_phase ^= 1;
           sb ^= 1;
           if (sb == 0) ug_phase ^= 1;
         }

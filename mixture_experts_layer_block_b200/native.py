@@ -66,6 +66,15 @@ class moe_ffn_grads(ctypes.Structure):
     _fields_ = [("up", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("down", ctypes.c_void_p)]
 
 
+class moe_int4_mat(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class moe_int4_experts(ctypes.Structure):
+    _fields_ = [(n, moe_int4_mat) for n in ("up", "gate", "down", "shared_up", "shared_gate", "shared_down")] + \
+               [("group", ctypes.c_int32), ("zeros", ctypes.c_int32)]
+
+
 # every symbol the header declares, with its C signature
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 SIGNATURES = {
@@ -82,6 +91,14 @@ SIGNATURES = {
     "moe_mxfp8_scale_bytes": (_I64, [_I64, _I64]),
     "moe_quantize_mxfp8": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P]),
     "moe_forward_mxfp8": (ctypes.c_int, [_P, _P, _I32, _P, _P, ctypes.POINTER(moe_mxfp8_experts), _I32, _P, _P]),
+    "moe_int4_code_bytes": (_I64, [_I64, _I64]),
+    "moe_int4_scale_bytes": (_I64, [_I64, _I64, _I32, _I32]),
+    "moe_quantize_int4": (ctypes.c_int, [_P, _P, _I64, _I64, _I32, _I32, _P, _P, _P]),
+    "moe_pack_int4": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I32, _P, _P, _P]),
+    "moe_matvec_int4": (ctypes.c_int, [_P, _P, _I64, ctypes.POINTER(moe_int4_mat), _I64, _I64, _I32, _I32, _P, _I32,
+                                       _P]),
+    "moe_experts_int4": (ctypes.c_int, [_P, _P, _I32, _P, _P, _I32, ctypes.POINTER(moe_int4_experts), _P, _I32, _P]),
+    "moe_forward_int4": (ctypes.c_int, [_P, _P, _I32, _P, _P, ctypes.POINTER(moe_int4_experts), _I32, _P, _P]),
     "moe_ffn_workspace_bytes": (_I64, [_I64, _I32, _I32, _I32]),
     "moe_ffn_forward": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, ctypes.POINTER(moe_shared_w), _P, _I32, _P, _P,
                                        _P, _I64, _P]),
@@ -202,6 +219,23 @@ def _raw_stream(stream, device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+class Int4Matrix:
+    """A matrix [rows, cols] in 4 bits, in the library's layout (include/moe_b200.h): its codes and
+    scales as uint8 CUDA tensors. Made by MoELayer.quantize_int4 or MoELayer.pack_int4."""
+    __slots__ = ("codes", "scales", "rows", "cols", "group", "zeros", "c")
+
+    def __init__(self, rows, cols, group, zeros, device):
+        import torch
+        nc, ns = lib.moe_int4_code_bytes(rows, cols), lib.moe_int4_scale_bytes(rows, cols, group, 1 if zeros else 0)
+        if nc < 0 or ns < 0:
+            raise ValueError("4-bit matrices have columns in a multiple of 8 and groups of 32, 64 or 128 columns: "
+                             f"got {rows}x{cols} with groups of {group}")
+        self.codes = torch.empty(nc, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(ns, dtype=torch.uint8, device=device)
+        self.rows, self.cols, self.group, self.zeros = rows, cols, group, bool(zeros)
+        self.c = moe_int4_mat(self.codes.data_ptr(), self.scales.data_ptr())
+
+
 class MoELayer:
     """Owns one moe_handle. Tensors are torch CUDA tensors laid out as include/moe_b200.h
     states (x [T,H] bf16, W_router [E,H], W_up/W_gate [E,D,H], W_down [E,H,D] bf16, bias [E]
@@ -275,6 +309,120 @@ class MoELayer:
                                          top_k or self.cfg.top_k, _ptr(out_host), _stream(stream)),
               "moe_forward_host_async")
         return out_host
+
+    # ---- 4-bit weights ----
+    def quantize_int4(self, src, group=128, zeros=False, stream=None):
+        """moe_quantize_int4 of a bf16 CUDA matrix [R, K] (a 3-D tensor is viewed as [-1, K])."""
+        m = src.reshape(-1, src.shape[-1])
+        _is_tensor(m, "src", m.shape, _BF16, self.device)
+        out = self._int4_matrix(m.shape[0], m.shape[1], group, zeros, stream)
+        check(lib.moe_quantize_int4(self.h, m.data_ptr(), out.rows, out.cols, group, 1 if zeros else 0, out.c.codes,
+                                    out.c.scales, _raw_stream(stream, self.device)), "moe_quantize_int4")
+        return out
+
+    def pack_int4(self, q, scales, zeros=None, group=128, stream=None):
+        """moe_pack_int4: the library's layout of a matrix quantised elsewhere. q uint8 [R, K/2] (the
+        even column in a byte's low half), scales bf16 [R, ceil(K/group)], zeros uint8 like scales
+        or None."""
+        if getattr(q, "ndim", 0) != 2:
+            raise ValueError("q must be [R, K / 2]")
+        rows, cols = q.shape[0], 2 * q.shape[1]
+        out = self._int4_matrix(rows, cols, group, zeros is not None, stream)
+        _is_tensor(q, "q", (rows, cols // 2), _U8, self.device)
+        _is_tensor(scales, "scales", (rows, -(-cols // group)), _BF16, self.device)
+        if zeros is not None:
+            _is_tensor(zeros, "zeros", (rows, -(-cols // group)), _U8, self.device)
+        check(lib.moe_pack_int4(self.h, q.data_ptr(), scales.data_ptr(), _addr(zeros), rows, cols, group, out.c.codes,
+                                out.c.scales, _raw_stream(stream, self.device)), "moe_pack_int4")
+        return out
+
+    def _int4_matrix(self, rows, cols, group, zeros, stream):
+        import torch
+        if stream is None:
+            return Int4Matrix(rows, cols, group, zeros, torch.device("cuda", self.device))
+        with torch.cuda.stream(stream):
+            return Int4Matrix(rows, cols, group, zeros, torch.device("cuda", self.device))
+
+    def quantize_experts_int4(self, wts, group=128, zeros=False, stream=None):
+        """The experts of a weight dict (W_up, W_gate, W_down and, with a shared expert, Ws_up, Ws_gate,
+        Ws_down) as {name: Int4Matrix}."""
+        names = ["W_up", "W_gate", "W_down"] + (["Ws_up", "Ws_gate", "Ws_down"] if wts.get("Ws_up") is not None else [])
+        return {n: self.quantize_int4(wts[n], group, zeros, stream) for n in names}
+
+    def matvec_int4(self, x, w, out, stream=None):
+        """moe_matvec_int4: out [T, rows] (bf16 or fp32) = x [T, cols] (bf16) times the Int4Matrix w."""
+        if not isinstance(w, Int4Matrix):
+            raise TypeError(f"w must be an Int4Matrix, got {type(w).__name__}")
+        if getattr(x, "ndim", 0) != 2:
+            raise ValueError("x must be [T, cols]")
+        T = x.shape[0]
+        _is_tensor(x, "x", (T, w.cols), _BF16, self.device)
+        _is_tensor(out, "out", (T, w.rows), _BF16_F32, self.device)
+        if w.codes.get_device() != self.device:
+            raise ValueError(f"w must be on cuda:{self.device}, got {w.codes.device}")
+        check(lib.moe_matvec_int4(self.h, x.data_ptr(), T, w.c, w.rows, w.cols, w.group, 1 if w.zeros else 0,
+                                  out.data_ptr(), 1 if out.element_size() == 2 else 0, _raw_stream(stream, self.device)),
+              "moe_matvec_int4")
+        return out
+
+    def _int4_experts(self, wq):
+        """The C struct of {name: Int4Matrix}, each checked against the layer's sizes."""
+        cfg = self.cfg
+        H, D, E, Ds = cfg.hidden, cfg.inter, cfg.num_experts, cfg.inter_shared
+        shapes = {"W_up": (E * D, H), "W_gate": (E * D, H), "W_down": (E * H, D)}
+        if Ds > 0:
+            shapes.update(Ws_up=(Ds, H), Ws_gate=(Ds, H), Ws_down=(H, Ds))
+        first = wq.get("W_up")
+        mats = []
+        for n in ("W_up", "W_gate", "W_down", "Ws_up", "Ws_gate", "Ws_down"):
+            if n not in shapes:
+                mats.append(moe_int4_mat())
+                continue
+            w = wq.get(n)
+            if not isinstance(w, Int4Matrix):
+                raise TypeError(f"{n} must be an Int4Matrix, got {type(w).__name__}")
+            if (w.rows, w.cols) != shapes[n]:
+                raise ValueError(f"{n} must be {shapes[n][0]}x{shapes[n][1]}, got {w.rows}x{w.cols}")
+            if w.group != first.group or w.zeros != first.zeros:
+                raise ValueError("the experts' matrices must share their group size, and have zero points or none")
+            if w.codes.get_device() != self.device:
+                raise ValueError(f"{n} must be on cuda:{self.device}, got {w.codes.device}")
+            mats.append(w.c)
+        return moe_int4_experts(*mats, first.group, 1 if first.zeros else 0)
+
+    def experts_int4(self, x, topk_ids, topk_w, wq, out, stream=None):
+        """moe_experts_int4: the layer behind its gating. x [T, H] bf16 (T <= 16), topk_ids [T, k]
+        int32, topk_w [T, k] fp32, wq {name: Int4Matrix} as quantize_experts_int4 returns, out [T, H]
+        bf16 or fp32."""
+        w = self._int4_experts(wq)
+        if getattr(x, "ndim", 0) != 2 or getattr(topk_ids, "ndim", 0) != 2:
+            raise ValueError("x must be [T, H] and topk_ids [T, k]")
+        T, k = topk_ids.shape
+        _is_tensor(x, "x", (T, self.cfg.hidden), _BF16, self.device)
+        _is_tensor(topk_ids, "topk_ids", (T, k), ("int32",), self.device)
+        _is_tensor(topk_w, "topk_w", (T, k), _F32, self.device)
+        _is_tensor(out, "out", (T, self.cfg.hidden), _BF16_F32, self.device)
+        check(lib.moe_experts_int4(self.h, x.data_ptr(), T, topk_ids.data_ptr(), topk_w.data_ptr(), k, w,
+                                   out.data_ptr(), 1 if out.element_size() == 2 else 0,
+                                   _raw_stream(stream, self.device)), "moe_experts_int4")
+        return out
+
+    def forward_int4(self, x, w_router, bias, wq, out, top_k=None, stream=None):
+        """moe_forward_int4: wq as quantize_experts_int4 returns; out in the handle's dtype."""
+        w = self._int4_experts(wq)
+        E, H = self.cfg.num_experts, self.cfg.hidden
+        if getattr(x, "ndim", 0) != 2:
+            raise ValueError("x must be [T, H]")
+        T = x.shape[0]
+        _is_tensor(x, "x", (T, H), _BF16, self.device)
+        _is_tensor(w_router, "w_router", (E, H), _BF16, self.device)
+        if bias is not None:
+            _is_tensor(bias, "bias", (E,), _F32, self.device)
+        _is_tensor(out, "out", (T, H), (self.out_dtype,), self.device)
+        check(lib.moe_forward_int4(self.h, x.data_ptr(), T, w_router.data_ptr(), _addr(bias), w,
+                                   top_k or self.cfg.top_k, out.data_ptr(), _raw_stream(stream, self.device)),
+              "moe_forward_int4")
+        return out
 
     # ---- the gated feed-forward block ----
     def _ffn_call(self, x, wts):

@@ -1,0 +1,392 @@
+"""4-bit weights on the GPU: the quantiser and the layout bit for bit, and the products (one matrix,
+the routed experts, the whole layer for a decode batch) against fp64 of the same quantised values.
+
+Bounds are derived: a rounding to bf16 is off by at most 2^-8 of the value; an fp32 sum of K
+products by at most K 2^-23 of the sum of their magnitudes (twice the bound of rounding to nearest,
+for additions that truncate; the group scales' multiplications, one per 32 columns or more, are
+within it too); the activation by 2^-18 |g| (1 + |u|), as for the bf16 block. Codes less their zero points
+are exact in bf16, so nothing else is rounded.
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+R16 = 2.0 ** -8
+R32 = 2.0 ** -23
+ACT = 2.0 ** -18
+
+
+def _layer(H=256, D=128, E=8, k=2, T=16, **kw):
+    from mixture_experts_layer_block_b200.native import MoELayer
+    return MoELayer(H, D, E, k, 16, T, **kw)
+
+
+def _checkpoint(R, K, group, zeros, seed):
+    """Codes two to a byte, bf16 scales and zero points, with every code and extreme among them."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(0, 16, (R, K), generator=g, dtype=torch.uint8)
+    G = -(-K // group)
+    s = (torch.rand(R, G, generator=g) * 0.9 + 0.1).mul(2.0 / K ** 0.5).to(torch.bfloat16)
+    s[R // 2] *= -1  # a negative scale is a scale
+    z = torch.randint(0, 16, (R, G), generator=g, dtype=torch.uint8) if zeros else None
+    return q, s, z
+
+
+def _values(q, s, z, group):
+    at = torch.arange(q.shape[1]) // group
+    return (q.double() - (8.0 if z is None else z.double()[:, at])) * s.double()[:, at]
+
+
+def _pack(layer, q, s, z, group):
+    p = (q[:, 0::2] | (q[:, 1::2] << 4)).contiguous()
+    return layer.pack_int4(p.cuda(), s.cuda(), None if z is None else z.cuda(), group)
+
+
+def _unpack(m):
+    """(codes [R, K], scales [R, G] as bf16 bits, zeros [R, G] or None) by the header's layout."""
+    R, K, G = m.rows, m.cols, -(-m.cols // m.group)
+    nb = -(-K // 64)
+    w = m.codes.cpu().numpy().view(np.uint32).reshape(-1, nb, 8, 4, 2, 2)  # tile, block, i, j, h, m
+    code = np.zeros((w.shape[0], 16, nb, 64), dtype=np.uint8)
+    where = [(0, 0), (8, 0), (0, 2), (8, 2), (0, 1), (8, 1), (0, 3), (8, 3)]
+    for i in range(8):
+        for j in range(4):
+            for h in range(2):
+                for mm in range(2):
+                    for n, (dr, dk) in enumerate(where):
+                        code[:, i + dr, :, 32 * h + 8 * j + 4 * mm + dk] = w[:, :, i, j, h, mm] >> (4 * n) & 15
+    code = code.reshape(-1, nb * 64)
+    order = [r for p in range(8) for r in (p, p + 8)]
+    e = m.scales.cpu().numpy().view(np.uint32 if m.zeros else np.uint16).reshape(-1, G, 16)
+    rows = np.empty_like(e)
+    rows[:, :, order] = e
+    rows = rows.transpose(0, 2, 1).reshape(-1, G)
+    zero = None
+    if m.zeros:
+        zero = torch.from_numpy((rows >> 16).astype(np.uint16).view(np.int16)).view(torch.bfloat16).float().numpy() - 128
+    return code, (rows & 0xffff).astype(np.uint16), zero
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("R,K", [(1, 8), (16, 64), (33, 328), (130, 2056)])
+def test_pack_layout(R, K, group, zeros):
+    layer = _layer()
+    q, s, z = _checkpoint(R, K, group, zeros, seed=R + K)
+    code, sb, zero = _unpack(_pack(layer, q, s, z, group))
+    np.testing.assert_array_equal(code[:R, :K], q.numpy())
+    assert not code[R:].any() and not code[:, K:].any()
+    np.testing.assert_array_equal(sb[:R], s.view(torch.int16).numpy().view(np.uint16))
+    if zeros:
+        np.testing.assert_array_equal(zero[:R], z.numpy())
+    layer.close()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("R,K", [(3, 8), (48, 1024), (50, 2088)])
+def test_quantize_bit_for_bit(R, K, group, zeros):
+    layer = _layer()
+    g = torch.Generator().manual_seed(R * K + group)
+    G = -(-K // group)
+    v = torch.randn(R, K, generator=g) * torch.exp2(torch.randint(-60, 60, (R, 1), generator=g).float())
+    v[0, :] = 0.0                  # a row of zeros
+    v[1, : min(K, 40)] = 1e-39     # scales that underflow or nearly do
+    v[2] = v[2].abs()              # one sign
+    v = v.to(torch.bfloat16)
+    m = layer.quantize_int4(v.cuda(), group, zeros)
+    code, sb, zero = _unpack(m)
+    f = torch.zeros(R, G * group)
+    f[:, :K] = v.float()
+    f = f.view(R, G, group)
+    mn, mx = f.amin(2).clamp(max=0), f.amax(2).clamp(min=0)
+    s = ((mx - mn) / 15 if zeros else f.abs().amax(2) / 7).to(torch.bfloat16)
+    sf = s.float()
+    ok = sf > 0
+    z = torch.where(ok, torch.round(-mn / sf).clamp(0, 15), torch.tensor(8.0)) if zeros else torch.full_like(sf, 8.0)
+    q = torch.where(ok[..., None], (torch.round(f / sf[..., None]) + z[..., None]).clamp(0, 15), torch.tensor(8.0))
+    np.testing.assert_array_equal(sb[:R], s.view(torch.int16).numpy().view(np.uint16))
+    np.testing.assert_array_equal(code[:R, :K], q.view(R, -1)[:, :K].numpy())
+    if zeros:
+        np.testing.assert_array_equal(zero[:R], z.numpy())
+    layer.close()
+
+
+def _close(got, ref, err, name=""):
+    err = err + (R16 * (ref.abs() + err) if got.dtype == torch.bfloat16 else 0) + 1e-30
+    bad = ~((got.double() - ref).abs() <= err)
+    assert not bool(bad.any()), (name, int(bad.sum()), float(((got.double() - ref).abs() / err).max()))
+
+
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 16, 37])
+@pytest.mark.parametrize("R,K,group,zeros", [(1, 8, 32, False), (40, 72, 64, True), (257, 2056, 128, False),
+                                             (512, 1024, 32, True), (2048, 328, 128, True), (4800, 520, 64, False),
+                                             (17, 7168, 32, False)])
+def test_matvec(T, R, K, group, zeros):
+    layer = _layer()
+    q, s, z = _checkpoint(R, K, group, zeros, seed=R)
+    m = _pack(layer, q, s, z, group)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16).cuda()
+    w = _values(q, s, z, group).cuda()
+    ref = x.double() @ w.T
+    err = (K + 8) * R32 * (x.double().abs() @ w.abs().T)
+    for dtype in (torch.float32, torch.bfloat16):
+        buf = torch.full((T + 2, R), 7.0, dtype=dtype, device="cuda")
+        layer.matvec_int4(x, m, buf[1:T + 1])
+        _close(buf[1:T + 1], ref, err)
+        assert bool((buf[0] == 7).all()) and bool((buf[T + 1] == 7).all())
+    layer.close()
+
+
+def _experts(H, D, E, Ds, group, zeros, seed, layer):
+    shapes = {"W_up": (E * D, H), "W_gate": (E * D, H), "W_down": (E * H, D)}
+    if Ds:
+        shapes.update(Ws_up=(Ds, H), Ws_gate=(Ds, H), Ws_down=(H, Ds))
+    val, packed = {}, {}
+    for i, (n, (R, K)) in enumerate(shapes.items()):
+        q, s, z = _checkpoint(R, K, group, zeros, seed + i)
+        packed[n] = _pack(layer, q, s, z, group)
+        val[n] = _values(q, s, z, group).cuda()
+    return val, packed
+
+
+def _block(x, up, gate, down):
+    """(W_down SwiGLU(W_up x, W_gate x), its error bound) of one token in fp64."""
+    H, D = up.shape[1], up.shape[0]
+    u, g = up @ x, gate @ x
+    eu, eg = H * R32 * (up.abs() @ x.abs()), H * R32 * (gate.abs() @ x.abs())
+    s = torch.sigmoid(u)
+    h = u * s * g
+    eh = 1.1 * g.abs() * eu + (u * s).abs() * eg + eu * eg + ACT * g.abs() * (1 + u.abs())
+    eh = eh + R16 * (h.abs() + eh)
+    return down @ h, down.abs() @ eh + (D + 8) * R32 * (down.abs() @ h.abs())
+
+
+def _reference(x, ids, w, val, H, D, E, Ds):
+    T, k = ids.shape
+    out = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    err, size = torch.zeros_like(out), torch.zeros_like(out)
+    for t in range(T):
+        terms = [(int(e), float(p)) for e, p in zip(ids[t].tolist(), w[t].tolist()) if 0 <= e < E]
+        for e, p in terms:
+            y, ey = _block(x[t].double(), val["W_up"][e * D:(e + 1) * D], val["W_gate"][e * D:(e + 1) * D],
+                           val["W_down"][e * H:(e + 1) * H])
+            out[t] += p * y
+            err[t] += abs(p) * ey
+            size[t] += abs(p) * y.abs()
+        if Ds:
+            y, ey = _block(x[t].double(), val["Ws_up"], val["Ws_gate"], val["Ws_down"])
+            out[t] += y
+            err[t] += ey
+            size[t] += y.abs()
+    return out, err + (k + 16) * R32 * size
+
+
+CASES = [(1, 256, 128, 8, 2, 0, 128, False), (16, 256, 128, 8, 2, 64, 32, True), (7, 272, 48, 5, 3, 0, 64, False),
+         (16, 528, 272, 300, 8, 144, 128, True), (9, 1024, 512, 32, 32, 0, 32, False), (8, 64, 1040, 3, 1, 0, 64, True)]
+
+
+@pytest.mark.parametrize("T,H,D,E,k,Ds,group,zeros", CASES)
+def test_experts(T, H, D, E, k, Ds, group, zeros):
+    layer = _layer(H, D, E, k, inter_shared=Ds)
+    val, packed = _experts(H, D, E, Ds, group, zeros, H + D, layer)
+    g = torch.Generator().manual_seed(T * E)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32).cuda()
+    w = torch.softmax(torch.randn(T, k, generator=g), 1).cuda()
+    ref, err = _reference(x, ids, w, val, H, D, E, Ds)
+    for dtype in (torch.float32, torch.bfloat16):
+        buf = torch.full((T + 2, H), 7.0, dtype=dtype, device="cuda")
+        layer.experts_int4(x, ids, w, packed, buf[1:T + 1])
+        _close(buf[1:T + 1], ref, err)
+        assert bool((buf[0] == 7).all()) and bool((buf[T + 1] == 7).all())
+        again = torch.empty(T, H, dtype=dtype, device="cuda")
+        layer.experts_int4(x, ids, w, packed, again)
+        assert torch.equal(again, buf[1:T + 1])
+    layer.close()
+
+
+@pytest.mark.parametrize("Ds", [0, 64])
+def test_experts_with_dropped_and_repeated_slots(Ds):
+    """Ids outside [0, E) contribute nothing (a token may have none left), an expert named twice by a
+    token counts twice, and one expert may take every token."""
+    T, H, D, E, k = 12, 256, 128, 8, 4
+    layer = _layer(H, D, E, k, inter_shared=Ds)
+    val, packed = _experts(H, D, E, Ds, 64, True, 5, layer)
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    w = torch.rand(T, k, generator=g).cuda()
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    ids[0] = -1
+    ids[1] = torch.tensor([3, 3, 3, 3])
+    ids[2] = torch.tensor([E, 2, -5, 2 ** 30])
+    ids[3:, 0] = 6
+    ids = ids.cuda()
+    out = torch.full((T, H), float("nan"), device="cuda")
+    layer.experts_int4(x, ids, w, packed, out)
+    ref, err = _reference(x, ids, w, val, H, D, E, Ds)
+    _close(out, ref, err)
+    if not Ds:
+        assert bool((out[0] == 0).all())
+    ids.fill_(-1)  # nobody hits anything
+    layer.experts_int4(x, ids, w, packed, out)
+    ref, err = _reference(x, ids, w, val, H, D, E, Ds)
+    _close(out, ref, err)
+    layer.close()
+
+
+def test_bad_values_stay_with_their_token_and_expert():
+    """A NaN token spoils its own row; an expert whose scales are infinite spoils only the tokens that
+    it serves."""
+    T, H, D, E, k = 10, 256, 128, 6, 2
+    layer = _layer(H, D, E, k)
+    val, packed = _experts(H, D, E, 0, 32, False, 50, layer)
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    ids = torch.stack([torch.randperm(E - 1, generator=g)[:k] for _ in range(T)]).to(torch.int32).cuda()
+    ids[4, 1] = E - 1
+    w = torch.rand(T, k, generator=g).cuda()
+    clean = torch.empty(T, H, device="cuda")
+    layer.experts_int4(x, ids, w, packed, clean)
+    x2 = x.clone()
+    x2[7, 3] = float("nan")
+    q, s, z = _checkpoint(E * D, H, 32, False, 50)
+    s[(E - 1) * D:] = float("inf")
+    bad = dict(packed, W_up=_pack(layer, q, s, z, 32))
+    out = torch.empty(T, H, device="cuda")
+    layer.experts_int4(x2, ids, w, bad, out)
+    keep = [t for t in range(T) if t not in (4, 7)]
+    assert torch.equal(out[keep], clean[keep])
+    assert bool(torch.isnan(out[7]).any()) and not bool(torch.isfinite(out[4]).all())
+    layer.close()
+
+
+@pytest.mark.parametrize("flags,bias,cf", [(0, True, 0.0), (32, False, 0.0), (0, True, 1.0)])
+@pytest.mark.parametrize("T", [1, 11, 16])
+def test_forward_int4(T, flags, bias, cf):
+    """The layer: routing as moe_router_logits and moe_gate_topk give it, then the experts; with a
+    capacity, an expert takes its lowest tokens only."""
+    H, D, E, k, Ds = 256, 128, 8, 2, 64
+    layer = _layer(H, D, E, k, inter_shared=Ds, flags=flags, capacity_factor=cf)
+    val, packed = _experts(H, D, E, Ds, 128, False, 70, layer)
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    wr = (torch.randn(E, H, generator=g) * 0.1).to(torch.bfloat16).cuda()
+    b = torch.randn(E, generator=g).cuda() if bias else None
+    out = torch.empty(T, H, dtype=getattr(torch, layer.out_dtype), device="cuda")
+    layer.forward_int4(x, wr, b, packed, out)
+    logits = torch.empty(T, E, device="cuda")
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    layer.router_logits(x, wr, b, logits)
+    layer.gate_topk(logits, k, ids, w)
+    if cf:
+        cap = -(-T * k // E)
+        kept = ids.cpu().clone()
+        for e in range(E):
+            hit = [(t, j) for t in range(T) for j in range(k) if int(ids[t, j]) == e]
+            for t, j in hit[cap:]:
+                kept[t, j] = -1
+        ids = kept.cuda()
+    ref, err = _reference(x, ids, w, val, H, D, E, Ds)
+    # the K-split router of the forward and the stage call's differ in the logits' last bits:
+    # an fp32 dot product's bound (H 2^-23 of its terms' magnitudes, both sides) moves a softmax
+    # weight by at most twice that of itself
+    el = 4 * H * R32 * float((x.double().abs() @ wr.double().abs().T).max())
+    err = err + 2 * el * sum(v.abs() for v in [ref]) + 2 * el * _reference(x, ids, w.abs(), val, H, D, E, 0)[0].abs()
+    _close(out, ref, err)
+    assert layer.status() == (0, 0)
+    layer.close()
+
+
+def test_forward_int4_close_to_the_bf16_layer():
+    """Quantise the layer's experts and run both: the 4-bit layer is the bf16 layer on rounded
+    weights, so it equals a bf16 forward of the dequantised weights (exact in bf16 here: power-of-two
+    scales) up to the bf16 path's own roundings."""
+    H, D, E, k, T = 256, 128, 8, 2, 16
+    layer = _layer(H, D, E, k, flags=1024)
+    g = torch.Generator().manual_seed(4)
+    wts, packed = {}, {}
+    for n, (R, K, s3) in {"W_up": (E * D, H, (E, D, H)), "W_gate": (E * D, H, (E, D, H)), "W_down": (E * H, D, (E, H, D))}.items():
+        q = torch.randint(0, 16, (R, K), generator=g, dtype=torch.uint8)
+        s = torch.full((R, -(-K // 64)), 2.0 ** -6).to(torch.bfloat16)
+        packed[n] = _pack(layer, q, s, None, 64)
+        wts[n] = _values(q, s, None, 64).to(torch.bfloat16).cuda().view(s3)
+    wts["W_router"] = (torch.randn(E, H, generator=g) * 0.1).to(torch.bfloat16).cuda()
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    a, b = torch.empty(T, H, device="cuda"), torch.empty(T, H, device="cuda")
+    layer.forward(x, wts, a)
+    layer.forward_int4(x, wts["W_router"], None, packed, b)
+    d = layer.router_logits(x, wts["W_router"], None, torch.empty(T, E, device="cuda"))
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    layer.gate_topk(d, k, ids, w)
+    val = {n: wts[n].double().view(-1, wts[n].shape[-1]) for n in ("W_up", "W_gate", "W_down")}
+    ref, err = _reference(x, ids, w, val, H, D, E, 0)
+    size = _reference(x, ids, w.abs(), val, H, D, E, 0)[1]
+    el = 4 * H * R32 * float((x.double().abs() @ wts["W_router"].double().abs().T).max())
+    slack = 2 * el * (ref.abs() + size) + 1e-6
+    assert bool(((b.double() - ref).abs() <= err + slack).all())
+    assert bool(((a.double() - ref).abs() <= err + slack + 2 * R16 * (ref.abs() + err) + R16 * size).all())
+    layer.close()
+
+
+def test_captured_and_replayed_on_another_stream():
+    T, H, D, E, k = 6, 256, 128, 16, 4
+    layer = _layer(H, D, E, k)
+    _, packed = _experts(H, D, E, 0, 128, False, 7, layer)
+    wr = torch.randn(E, H).mul(0.1).to(torch.bfloat16).cuda()
+    x = torch.randn(T, H).to(torch.bfloat16).cuda()
+    out, one, ref, ref1 = (torch.empty(T, H, device="cuda") for _ in range(4))
+    one = torch.empty(T, E * D, device="cuda")
+    ref1 = torch.empty_like(one)
+    layer.forward_int4(x, wr, None, packed, out)
+    layer.matvec_int4(x, packed["W_up"], one)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward_int4(x, wr, None, packed, out)
+        layer.matvec_int4(x, packed["W_up"], one)
+    for seed in (1, 2):
+        x.copy_(torch.randn(T, H, generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        layer.forward_int4(x, wr, None, packed, ref, stream=s)
+        layer.matvec_int4(x, packed["W_up"], ref1, stream=s)
+        s.synchronize()
+        assert torch.equal(out, ref) and torch.equal(one, ref1)
+    layer.close()
+
+
+def test_weights_packed_right_before_they_are_read():
+    """Laying out, quantising and reading follow one another on a stream: no product sees the buffers
+    of the matrix before."""
+    layer = _layer()
+    R, K, T = 2048, 512, 4
+    x = torch.randn(T, K).to(torch.bfloat16).cuda()
+    out = torch.empty(T, R, device="cuda")
+    got, refs = [], []
+    mats = [torch.randn(R, K, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in range(4)]
+    for m in mats:
+        got.append(layer.matvec_int4(x, layer.quantize_int4(m, 64), torch.empty_like(out)))
+    torch.cuda.synchronize()
+    for m in mats:
+        w = layer.quantize_int4(m, 64)
+        torch.cuda.synchronize()
+        refs.append(layer.matvec_int4(x, w, torch.empty_like(out)))
+    for a, b in zip(got, refs):
+        assert torch.equal(a, b)
+    layer.close()
+
+
+def test_no_tokens():
+    layer = _layer()
+    _, packed = _experts(256, 128, 8, 0, 64, False, 3, layer)
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(0, 256, device="cuda")
+    layer.matvec_int4(x, packed["W_up"], torch.empty(0, 8 * 128, device="cuda"))
+    layer.experts_int4(x, torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda"), packed, out)
+    layer.forward_int4(x, torch.zeros(8, 256, dtype=torch.bfloat16, device="cuda"), None, packed, out)
+    layer.close()
