@@ -3,8 +3,8 @@
 // What bounds them: the weights' bytes, each read once from HBM, and at the smallest sizes the
 // latency of one trip there. So the design is about bytes in flight and short dependent chains:
 //  - a unit is 16 output rows (for the experts: of one expert, or, in the down projection, of the sum
-//    over all experts that were hit); the CTA's 8 warps split its K blocks evenly, and the down
-//    projection's K runs over every expert hit, so that warps are even there too;
+//    over all experts that were hit); 1 to 16 warps split its K blocks evenly, as many as keep all
+//    warps of the GPU busy, and the down projection's K runs over every expert hit;
 //  - each lane copies its own 16-byte pieces of weights to shared memory with cp.async, a fixed number
 //    of blocks ahead and across unit boundaries, and reads only its own: no barrier in the K loop;
 //  - the products run on mma.sync m16n8k16 (fp32 accumulation): weights come out of a register
@@ -13,7 +13,7 @@
 //  - 4-bit codes become bf16 exactly: (code | 0x4300) is 128 + code, less bf16(128 + zero). A group's
 //    sum is scaled in fp32, so nothing is rounded before the result;
 //  - a kernel behind another of the same call starts copying weights before that one is done.
-// The warps' partial sums meet in shared memory and are added in warp order: equal inputs give equal
+// Partial sums of one unit meet in shared memory and are added in warp order: equal inputs give equal
 // bits.
 #include <algorithm>
 
@@ -25,8 +25,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kMvWarps = 8;
-constexpr int kMvThreads = kMvWarps * 32;
 constexpr int kMvSmem = 227 * 1024;      // shared memory of an SM that CTAs can use
 constexpr int kMvMaxDepth = 12;
 
@@ -35,9 +33,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 template <int kBytes>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool in) {
-  const uint32_t n = in ? (uint32_t)kBytes : 0u;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -59,403 +56,501 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The experts of a batch: which were hit, in rising order, and by which tokens.
+// The experts of a batch: which were hit, in rising order, by which tokens, and for every (expert,
+// token) pair, in that order, the token's router weight for that expert.
 struct Hits {
   int32_t n;
   uint16_t expert[kMvMaxSlots];
   uint16_t mask[kMvMaxSlots];
-  int16_t id[kMvMaxSlots];   // the caller's ids, -1 where they are out of range
-  float w[kMvMaxSlots];
+  uint16_t first[kMvMaxSlots];  // the expert's first pair
+  float weight[kMvMaxSlots];    // by pair: an expert that a token names twice counts twice
 };
+
+constexpr int kMvWarps = 16;  // one CTA to an SM
+constexpr int kMvThreads = kMvWarps * 32;
 
 template <bool kW4, bool kDual, int kKind, int kNT, bool kG32, bool kZeros>
 struct Mv {
   static constexpr int kMats = kDual ? 2 : 1;
-  static constexpr int kScaleBytes = kZeros ? 8 : 4;             // a lane's entries of a group: rows q and q + 8
-  static constexpr int kGroups = kG32 ? 2 : 1;                   // groups of a K block
-  static constexpr int kLane = kW4 ? 16 : 64;                    // weight bytes of a lane and block
-  static constexpr int kMetaLane = kW4 ? kScaleBytes * kGroups : 0;
-  static constexpr int kStage = kMats * 32 * (kLane + kMetaLane);  // bytes of a warp's block
+  static constexpr int kGroups = kG32 ? 2 : 1;                        // groups of a K block
+  static constexpr int kLane = kW4 ? 16 : 64;                         // weight bytes of a lane and block
+  static constexpr int kMeta = kW4 ? (kZeros ? 8 : 4) * kGroups : 0;  // scale bytes of a lane and block
+  static constexpr int kMat = 32 * (kLane + kMeta);                   // bytes of a warp's block of a matrix
+  static constexpr int kStage = kMats * kMat;
   static constexpr int kCols = kNT * 8;
-  static constexpr int kRedLd = kMvRows + 1;
-  static constexpr int kRed = kMats * kCols * kRedLd;            // floats of a warp's partial sums
-  static constexpr int kRest = 2 * kMvWarps * kRed * (int)sizeof(float) + (kKind != kMvOne ? (int)sizeof(Hits) : 0);
-  // two CTAs to an SM where each still gets 4 blocks a warp, else one
-  static constexpr int depth_of(int ctas) {
-    return std::min(kMvMaxDepth, (kMvSmem / ctas - 1024 - kRest) / (kMvWarps * kStage));
-  }
-  static constexpr int kPerSm = depth_of(2) >= 4 ? 2 : 1;
-  static constexpr int kDepth = depth_of(kPerSm);
+  static constexpr int kRed = kMats * kCols * kMvRows;                // floats of a warp's partial sums
+  static constexpr int kRest = kMvWarps * kRed * (int)sizeof(float) + (kKind != kMvOne ? (int)sizeof(Hits) : 0);
+  static constexpr int kDepth = std::min(kMvMaxDepth, (kMvSmem - 1024 - kRest) / (kMvWarps * kStage));
   static constexpr int kRingTotal = kMvWarps * kStage * kDepth;
   static constexpr int kSmem = kRingTotal + kRest;
-  static_assert(kDepth >= 3, "enough blocks in flight");
+  static_assert(kDepth >= 3, "two blocks in flight beside the one in use");
 };
 
-// A position in a warp's sequence of K blocks: its units, and in each the warp's share of blocks.
-struct Cursor {
-  int u;        // unit
-  int b, hi;    // block of the unit's K (all its experts), end of this warp's share
-  int ent;      // entry of the hit list (n: the shared expert)
-  int kb, nb;   // block of the entry's matrix, blocks it has
-  int tile;     // 16-row tile of the entry's matrix
+// Where a warp is in its sequence of K blocks: units of 16 output rows, in each a share of the unit's K
+// blocks, which run over one matrix or (kMvDown) over those of all experts hit. A segment is a run of
+// blocks of one matrix.
+struct Walk {
+  int u;      // unit
+  int left;   // blocks of this unit's share behind this segment
+  int n;      // blocks of this segment from here on (0 past the last unit)
+  int ent;    // the matrix: entry of the hit list (its length: the shared expert)
+  int kb;     // block of the matrix where the segment begins
 };
+
+// A sum's place in a warp's partial sums: 16 rows to a token, rotated so that the four tokens that a
+// quarter warp writes at once fall into different banks.
+__device__ __forceinline__ int red_at(int col, int row) { return col * kMvRows + ((row + 4 * (col >> 1)) & 15); }
 
 }  // namespace
 
 template <bool kW4, bool kDual, int kKind, int kNT, bool kG32, bool kZeros>
-__global__ void __launch_bounds__(kMvThreads, Mv<kW4, kDual, kKind, kNT, kG32, kZeros>::kPerSm)
-    mv_kernel(const __grid_constant__ MvArgs a) {
+__global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant__ MvArgs a) {
   using C = Mv<kW4, kDual, kKind, kNT, kG32, kZeros>;
+  constexpr int kThreads = kMvThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = lane >> 2, c = lane & 3;
   float* red = reinterpret_cast<float*>(smem + C::kRingTotal);
-  Hits* hits = reinterpret_cast<Hits*>(smem + C::kRingTotal + 2 * kMvWarps * C::kRed * sizeof(float));
-  uint8_t* ring = smem + (size_t)warp * C::kStage * C::kDepth;
+  Hits* hits = reinterpret_cast<Hits*>(smem + C::kRingTotal + kMvWarps * C::kRed * sizeof(float));
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * C::kStage * C::kDepth) + (uint32_t)lane * 16;
+  const uint8_t* ring_p = smem + (size_t)warp * C::kStage * C::kDepth;
 
   if (!a.early) griddep_wait();
   int nhit = 1;
   if constexpr (kKind != kMvOne) {
-    // the partial sums' buffer is free until the first unit: token masks by expert
+    // the partial sums' buffer is free until the first unit: the experts' token masks
     uint32_t* emask = reinterpret_cast<uint32_t*>(red);
-    static_assert(2 * kMvWarps * C::kRed * 4 >= kMaxExperts * 4, "the masks fit");
-    for (int e = threadIdx.x; e < a.E; e += kMvThreads) emask[e] = 0;
+    static_assert(kMvWarps * C::kRed * 4 >= kMaxExperts * 4, "the masks fit");
+    for (int e = threadIdx.x; e < a.E; e += kThreads) emask[e] = 0;
     __syncthreads();
-    for (int s = threadIdx.x; s < a.T * a.k; s += kMvThreads) {
+    for (int s = threadIdx.x; s < a.T * a.k; s += kThreads) {
       const int e = __ldcg(a.ids + s);
-      const bool in = e >= 0 && e < a.E;
-      hits->id[s] = in ? (int16_t)e : (int16_t)-1;
-      hits->w[s] = __ldcg(a.topk_w + s);
-      if (in) atomicOr(&emask[e], 1u << (s / a.k));
+      if (e >= 0 && e < a.E) atomicOr(&emask[e], 1u << (s / a.k));
     }
     __syncthreads();
     if (warp == 0) {
-      int n = 0;
+      int n = 0, pairs = 0;
       for (int e0 = 0; e0 < a.E; e0 += 32) {
         uint32_t m = e0 + lane < a.E ? emask[e0 + lane] : 0;
         if (a.capacity > 0)
           while (__popc(m) > a.capacity) m &= ~(0x80000000u >> __clz(m));  // the highest token is dropped
         const uint32_t any = __ballot_sync(0xffffffffu, m != 0);
+        if (any == 0) continue;
+        int sum = __popc(m);  // inclusive scan of the pairs
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
         if (m) {
           const int at = n + __popc(any & ((1u << lane) - 1));
           hits->expert[at] = (uint16_t)(e0 + lane);
           hits->mask[at] = (uint16_t)m;
+          hits->first[at] = (uint16_t)(pairs + sum - __popc(m));
         }
         n += __popc(any);
+        pairs += __shfl_sync(0xffffffffu, sum, 31);
       }
       if (lane == 0) hits->n = n;
     }
     __syncthreads();
     nhit = hits->n;
+    if constexpr (kKind == kMvDown) {
+      for (int i = threadIdx.x; i < nhit; i += kThreads) {
+        const int e = hits->expert[i];
+        int pair = hits->first[i];
+        for (uint32_t m = hits->mask[i]; m; m &= m - 1) {
+          const int t = __ffs(m) - 1;
+          float w = 0.f;
+          for (int j = 0; j < a.k; ++j)
+            if (__ldcg(a.ids + t * a.k + j) == e) w += __ldcg(a.topk_w + t * a.k + j);
+          hits->weight[pair++] = w;
+        }
+      }
+      __syncthreads();
+    }
   }
 
   const int tiles = ceil_div(a.m.R, kMvRows), nb = ceil_div(a.m.K, kMvBK);
   const int stiles = ceil_div(a.shared.R, kMvRows), snb = ceil_div(a.shared.K, kMvBK);
-  const int units = kKind == kMvOne ? tiles : (kKind == kMvUp ? nhit * tiles + stiles : tiles);
+  const int routed = kKind == kMvUp ? nhit * tiles : tiles;  // units of the routed experts
+  const int units = kKind == kMvUp ? routed + stiles : tiles;
 
-  auto start_entry = [&](Cursor& p) {  // kMvDown: the entry that block p.b belongs to
-    p.ent = min(p.b / max(nb, 1), nhit);
-    p.kb = p.b - p.ent * nb;
-    p.nb = p.ent == nhit ? snb : nb;
-  };
-  auto start_unit = [&](Cursor& p) {
-    while (p.u < units) {
-      int total;
+  // `wk` warps share a unit: as many as keep every warp busy
+  int wk = kMvWarps;
+  while (wk > 1 && (int64_t)units * wk > (int64_t)gridDim.x * kMvWarps) wk >>= 1;
+  const int group = warp / wk, part = warp - group * wk;  // groups of warps take units in turn
+  const int stride = gridDim.x * (kMvWarps / wk);
+
+  // The first segment of this warp's share of unit p.u, or of the next unit where it has one.
+  auto start_unit = [&](Walk& p) {
+    for (; p.u < units; p.u += stride) {
+      const bool sh = kKind == kMvUp && p.u >= routed;
+      const int total = kKind == kMvDown ? nhit * nb + snb : (sh ? snb : nb);
+      const int b = (int)((int64_t)part * total / wk), n = (int)((int64_t)(part + 1) * total / wk) - b;
+      if (n == 0) continue;  // fewer blocks than warps: nothing of this unit is this warp's
       if constexpr (kKind == kMvDown) {
-        p.tile = p.u;
-        total = nhit * nb + snb;
-      } else if constexpr (kKind == kMvUp) {
-        const bool sh = p.u >= nhit * tiles;
-        p.ent = sh ? nhit : p.u / tiles;
-        p.tile = sh ? p.u - nhit * tiles : p.u % tiles;
-        total = p.nb = sh ? snb : nb;
+        p.ent = min(b / nb, nhit);
+        p.kb = b - p.ent * nb;
+        p.n = min(n, (p.ent == nhit ? snb : nb) - p.kb);
       } else {
-        p.ent = 0;
-        p.tile = p.u;
-        total = p.nb = nb;
+        p.ent = kKind == kMvUp ? (sh ? nhit : p.u / tiles) : 0;
+        p.kb = b;
+        p.n = n;
       }
-      p.b = (int)((int64_t)warp * total / kMvWarps);
-      p.hi = (int)((int64_t)(warp + 1) * total / kMvWarps);
-      if (p.b < p.hi) {
-        if constexpr (kKind == kMvDown) start_entry(p);
-        else p.kb = p.b;
-        return;
-      }
-      p.u += gridDim.x;  // fewer blocks than warps: nothing of this unit is this warp's
+      p.left = n - p.n;
+      return;
     }
+    p.n = 0;
   };
-  auto advance = [&](Cursor& p) {
-    ++p.b;
-    ++p.kb;
-    if (p.b >= p.hi) {
-      p.u += gridDim.x;
+  auto next_segment = [&](Walk& p) {
+    if (kKind == kMvDown && p.left > 0) {
+      ++p.ent;
+      p.kb = 0;
+      p.n = min(p.left, p.ent == nhit ? snb : nb);
+      p.left -= p.n;
+    } else {
+      p.u += stride;
       start_unit(p);
-    } else if (kKind == kMvDown && p.kb == p.nb) {
-      start_entry(p);
     }
   };
 
-  // ---- weights: block `p` into ring slot `slot`, this lane's pieces only ----
-  auto copy = [&](const Cursor& p, int slot) {
-    const bool sh = kKind != kMvOne && p.ent == nhit;
+  // ---- weights: this lane's pieces of a block, from running addresses ----
+  Walk prod{};
+  prod.u = blockIdx.x + group * gridDim.x;
+  const uint8_t* wp[C::kMats];   // 4-bit: codes; bf16: row q
+  const uint8_t* sp[C::kMats];   // 4-bit: scales; bf16: row q + 8
+  bool in0 = true, in1 = true;   // bf16: rows q and q + 8 exist
+  int wcols = 0;                 // bf16: columns from this lane's first one to the end of the matrix
+  int half = 0;                  // 4-bit, groups of 128: the block's half of its group's columns
+  auto aim_weights = [&]() {
+    if (prod.n == 0) return;
+    const bool sh = kKind != kMvOne && prod.ent == nhit;
     const MvMatrix& m = sh ? a.shared : a.m;
-    const int e = kKind == kMvOne || sh ? 0 : hits->expert[p.ent];
-    const uint32_t dst = smem_u32(ring) + slot * C::kStage + lane * C::kLane;
+    const int e = kKind == kMvOne || sh ? 0 : hits->expert[prod.ent];
+    const int tile = kKind == kMvUp ? (sh ? prod.u - routed : prod.u - prod.ent * tiles) : prod.u;
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
-        const int64_t tile = (int64_t)e * int4_row_tiles(m.R) + p.tile;
-        const uint8_t* w = static_cast<const uint8_t*>(m.w[i]) + (tile * p.nb + p.kb) * 512 + lane * 16;
-        cp_async16(dst + i * 32 * C::kLane, w, true);
-        const int G = (m.K + a.group - 1) / a.group;
-        const uint32_t md = smem_u32(ring) + slot * C::kStage + C::kMats * 32 * C::kLane + i * 32 * C::kMetaLane +
-                            lane * C::kMetaLane;
-#pragma unroll
-        for (int g2 = 0; g2 < C::kGroups; ++g2) {
-          const int g = kG32 ? 2 * p.kb + g2 : (a.group == 64 ? p.kb : p.kb >> 1);
-          const bool in = g < G;
-          const uint8_t* s = static_cast<const uint8_t*>(m.scales[i]) +
-                             (tile * G + (in ? g : 0)) * (kMvRows * (kZeros ? 4 : 2)) + q * C::kScaleBytes;
-          cp_async_small<C::kScaleBytes>(md + g2 * C::kScaleBytes, s, in);
-        }
+        const int64_t at = (int64_t)e * ((m.R + kMvRows - 1) / kMvRows) + tile;
+        wp[i] = static_cast<const uint8_t*>(m.w[i]) + (at * (sh ? snb : nb) + prod.kb) * 512 + lane * 16;
+        // a copy brings a lane the entries of a whole K block (of two, with groups of 128)
+        const bool wide = !kG32 && a.group == 128;
+        const int per = wide ? (m.K + 127) >> 7 : (m.K + 63) >> 6;
+        sp[i] = static_cast<const uint8_t*>(m.scales[i]) + (at * per + (wide ? prod.kb >> 1 : prod.kb)) * (8 * C::kMeta) +
+                q * C::kMeta;
+        half = prod.kb & 1;
       } else {
+        const int row = tile * kMvRows + q;
+        in0 = row < m.R;
+        in1 = row + 8 < m.R;
         const uint16_t* w = static_cast<const uint16_t*>(m.w[i]);
-#pragma unroll
-        for (int r2 = 0; r2 < 2; ++r2) {
-          const int row = p.tile * kMvRows + q + 8 * r2;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k = p.kb * kMvBK + 32 * h + 8 * c;  // K is a multiple of 8
-            const bool in = row < m.R && k < m.K;
-            // the four pieces of a lane are 16 lanes' widths apart: conflict-free writes and reads
-            cp_async16(smem_u32(ring) + slot * C::kStage + (i * 4 + r2 * 2 + h) * 512 + lane * 16,
-                       in ? w + (int64_t)row * m.K + k : w, in);
-          }
-        }
+        const int64_t col = prod.kb * kMvBK + 8 * c;
+        wp[i] = reinterpret_cast<const uint8_t*>(w + (in0 ? (int64_t)row * m.K : 0) + col);
+        sp[i] = reinterpret_cast<const uint8_t*>(w + (in1 ? (int64_t)(row + 8) * m.K : 0) + col);
+        wcols = m.K - (int)col;
       }
     }
   };
+  auto copy = [&](uint32_t slot_off) {
+    const uint32_t dst = ring + slot_off;
+#pragma unroll
+    for (int i = 0; i < C::kMats; ++i) {
+      if constexpr (kW4) {
+        cp_async16(dst + i * C::kMat, wp[i], true);
+        wp[i] += 512;
+        cp_async_small<C::kMeta>(dst + i * C::kMat + 512 - lane * (16 - C::kMeta), sp[i]);
+        if (kG32 || a.group != 128 || half) sp[i] += 8 * C::kMeta;
+      } else {
+        // a piece outside the matrix is zeros; K is a multiple of 8, so that pieces are whole
+        const bool k0 = wcols > 0, k1 = wcols > 32;
+        cp_async16(dst + (i * 4 + 0) * 512, k0 ? wp[i] : static_cast<const uint8_t*>(a.m.w[i]), in0 && k0);
+        cp_async16(dst + (i * 4 + 1) * 512, k1 ? wp[i] + 64 : static_cast<const uint8_t*>(a.m.w[i]), in0 && k1);
+        cp_async16(dst + (i * 4 + 2) * 512, k0 ? sp[i] : static_cast<const uint8_t*>(a.m.w[i]), in1 && k0);
+        cp_async16(dst + (i * 4 + 3) * 512, k1 ? sp[i] + 64 : static_cast<const uint8_t*>(a.m.w[i]), in1 && k1);
+        wp[i] += 128;
+        sp[i] += 128;
+      }
+    }
+    if constexpr (kW4) half ^= 1;
+    else wcols -= kMvBK;
+    if (--prod.n == 0) {
+      next_segment(prod);
+      aim_weights();
+    }
+  };
 
-  // ---- activations: this lane's columns of block `p` for tokens q and q + 8 ----
-  auto load_x = [&](const Cursor& p, uint4 (&x)[kNT][2]) {
-    const bool sh = kKind != kMvOne && p.ent == nhit;
-    const int K = sh ? a.shared.K : a.m.K;
-    const uint32_t members = kKind == kMvOne || sh ? 0xffffu : hits->mask[p.ent];
+  // ---- activations: this lane's columns of a block for its tokens ----
+  // Tokens are the MMA's columns, in tiles of 8. Where an expert's tokens all lie in one of the two
+  // tiles, only that one is computed: `tile0` is the first tile with a token, `both` whether the
+  // other one has some too.
+  Walk nxt{};
+  const uint16_t* xp[kNT];       // null: not a token of this expert
+  int xk = 0;                    // columns from this lane's first one to the end
+  auto tokens_of = [&](int ent) -> uint32_t {
+    return kKind == kMvOne || ent == nhit ? (1u << a.T) - 1 : hits->mask[ent];
+  };
+  auto aim_x = [&]() {
+    if (nxt.n == 0) return;
+    const bool sh = kKind != kMvOne && nxt.ent == nhit;
+    const uint32_t members = tokens_of(nxt.ent);
+    const int tile0 = kNT == 2 && (members & 0xffu) == 0 ? 1 : 0;
+    const int col = nxt.kb * kMvBK + 8 * c;
+    xk = (sh ? a.shared.K : a.m.K) - col;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
-      const int t = q + 8 * n;
-      const bool in = t < a.T && (members >> t & 1);
+      const int t = q + 8 * (tile0 + n);
       int64_t row = t;
-      if constexpr (kKind == kMvDown) {
-        if (sh) {
-          row = (int64_t)a.T * a.k + t;
-        } else if (in) {
-          const int e = hits->expert[p.ent];
-          int j = 0;
-          while (j < a.k - 1 && hits->id[t * a.k + j] != e) ++j;
-          row = (int64_t)t * a.k + j;
-        }
-      }
+      if constexpr (kKind == kMvDown)  // h's rows
+        row = sh ? a.T * a.k + t : hits->first[nxt.ent] + __popc(members & ((1u << t) - 1));
+      xp[n] = t < 8 * kNT && (members >> t & 1) ? a.x + row * a.ldx + col : nullptr;
+    }
+  };
+  auto load_x = [&](uint4 (&x)[kNT][2]) {  // the next block's, if there is one
+    if (nxt.n == 0) return;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = p.kb * kMvBK + 32 * h + 8 * c;
-        // plain loads: the CTAs of an SM share the rows through L1
-        x[n][h] = in && k < K ? *reinterpret_cast<const uint4*>(a.x + row * a.ldx + k) : make_uint4(0, 0, 0, 0);
-      }
+    for (int n = 0; n < kNT; ++n) {
+      const bool in = xp[n] != nullptr;
+      // plain loads: the warps of an SM share the rows through L1
+      x[n][0] = in && xk > 0 ? *reinterpret_cast<const uint4*>(xp[n]) : make_uint4(0, 0, 0, 0);
+      x[n][1] = in && xk > 32 ? *reinterpret_cast<const uint4*>(xp[n] + 32) : make_uint4(0, 0, 0, 0);
+      if (in) xp[n] += kMvBK;
+    }
+    xk -= kMvBK;
+    if (--nxt.n == 0) {
+      next_segment(nxt);
+      aim_x();
     }
   };
 
-  Cursor prod{};
-  prod.u = blockIdx.x;
   start_unit(prod);
-  Cursor cur = prod, nxt = prod;
-  int slot_in = 0, slot = 0;
+  Walk cur = prod;
+  nxt = prod;
+  aim_weights();
+  uint32_t slot_in = 0, slot = 0;  // byte offsets of the ring's slots
 #pragma unroll 1
   for (int i = 0; i < C::kDepth - 1; ++i) {
-    if (prod.u < units) {
-      copy(prod, slot_in);
-      advance(prod);
-    }
+    if (prod.n) copy(slot_in);
     cp_async_commit();
-    if (++slot_in == C::kDepth) slot_in = 0;
+    slot_in += C::kStage;
   }
   if (a.early) griddep_wait();
   griddep_launch_dependents();
 
-  uint4 xn[kNT][2];
-  if (nxt.u < units) load_x(nxt, xn);
-  int parity = 0;
-#pragma unroll 1
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    float acc[C::kMats][kNT][4] = {};   // of the current expert
-    float tot[kNT][4] = {};             // kMvDown: router-weighted, over the experts so far
-    auto close_entry = [&](int ent) {
-      if constexpr (kKind == kMvDown) {
-        const bool sh = ent == nhit;
-        const uint32_t members = sh ? 0xffffu : hits->mask[ent];
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int t2 = 0; t2 < 2; ++t2) {
-            const int t = 8 * n + 2 * c + t2;
-            if (t < a.T && (members >> t & 1)) {
-              float w = sh ? 1.f : 0.f;
-              if (!sh) {  // an expert named twice counts twice
-                const int e = hits->expert[ent];
-                for (int j = 0; j < a.k; ++j)
-                  if (hits->id[t * a.k + j] == e) w += hits->w[t * a.k + j];
-              }
-              tot[n][t2] += w * acc[0][n][t2];
-              tot[n][2 + t2] += w * acc[0][n][2 + t2];
-            }
-            acc[0][n][t2] = acc[0][n][2 + t2] = 0.f;
-          }
-      }
-    };
-    while (cur.u == u) {
-      if (prod.u < units) {
-        copy(prod, slot_in);
-        advance(prod);
-      }
-      cp_async_commit();
-      if (++slot_in == C::kDepth) slot_in = 0;
-      uint4 x[kNT][2];
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        x[n][0] = xn[n][0];
-        x[n][1] = xn[n][1];
-      }
-      advance(nxt);
-      if (nxt.u < units) load_x(nxt, xn);
-      cp_async_wait<C::kDepth - 1>();
-      const uint8_t* st = ring + (size_t)slot * C::kStage;
-      if (++slot == C::kDepth) slot = 0;
-#pragma unroll
-      for (int i = 0; i < C::kMats; ++i) {
-        if constexpr (kW4) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(st + i * 32 * C::kLane + lane * 16);
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          const uint8_t* meta = st + C::kMats * 32 * C::kLane + (i * 32 + lane) * C::kMetaLane;
-#pragma unroll
-          for (int g2 = 0; g2 < C::kGroups; ++g2) {
-            float s0, s1;                            // rows q and q + 8
-            uint32_t z0 = 0x43084308u, z1 = z0;      // bf16x2 of 128 + zero
-            if constexpr (kZeros) {
-              const uint2 v = *reinterpret_cast<const uint2*>(meta + g2 * 8);
-              s0 = __uint_as_float(v.x << 16);
-              s1 = __uint_as_float(v.y << 16);
-              z0 = __byte_perm(v.x, 0, 0x3232);
-              z1 = __byte_perm(v.y, 0, 0x3232);
-            } else {
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(meta + g2 * 4);
-              s0 = __uint_as_float(v << 16);
-              s1 = __uint_as_float(v & 0xffff0000u);
-            }
-            float part[kNT][4] = {};
-#pragma unroll
-            for (int jj = 0; jj < 4 / C::kGroups; ++jj) {
-              const int j = g2 * 2 * (C::kGroups - 1) + jj;
-              uint32_t f[4];
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                f[n] = sub_bf16x2(((w[j] >> (4 * n)) & 0x000f000fu) | 0x43004300u, (n & 1) ? z1 : z0);
-#pragma unroll
-              for (int n = 0; n < kNT; ++n) {
-                const uint4 v = x[n][j >> 1];
-                if (j & 1) mma_bf16(part[n], f, v.z, v.w);
-                else mma_bf16(part[n], f, v.x, v.y);
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-              acc[i][n][0] += s0 * part[n][0];
-              acc[i][n][1] += s0 * part[n][1];
-              acc[i][n][2] += s1 * part[n][2];
-              acc[i][n][3] += s1 * part[n][3];
-            }
-          }
+  float acc[C::kMats][kNT][4];   // of the current matrix
+  float tot[kNT][4];             // kMvDown: router-weighted, over the experts so far
+  uint32_t members = 0;
+  int tile0 = 0;
+  bool both = kNT == 2;
+  // One block: the copy of a later one, the next one's activations, and its products.
+  auto block = [&](const uint4 (&x)[kNT][2], uint4 (&xnext)[kNT][2]) {
+    if (prod.n) copy(slot_in);
+    cp_async_commit();
+    slot_in += C::kStage;
+    if (slot_in == C::kStage * C::kDepth) slot_in = 0;
+    load_x(xnext);
+    cp_async_wait<C::kDepth - 1>();
+    const uint8_t* st = ring_p + slot;
+    slot += C::kStage;
+    if (slot == C::kStage * C::kDepth) slot = 0;
+    #pragma unroll
+    for (int i = 0; i < C::kMats; ++i) {
+      if constexpr (kW4) {
+        const uint4 w4 = *reinterpret_cast<const uint4*>(st + i * C::kMat + lane * 16);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        const uint8_t* meta = st + i * C::kMat + 512 + lane * C::kMeta;
+        uint32_t mv[C::kMeta / 4];
+        if constexpr (C::kMeta == 16) {
+          const uint4 v = *reinterpret_cast<const uint4*>(meta);
+          mv[0] = v.x; mv[1] = v.y; mv[2] = v.z; mv[3] = v.w;
+        } else if constexpr (C::kMeta == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(meta);
+          mv[0] = v.x; mv[1] = v.y;
         } else {
-          uint4 w[2][2];  // rows q, q + 8; halves of the block
+          mv[0] = *reinterpret_cast<const uint32_t*>(meta);
+        }
 #pragma unroll
-          for (int r2 = 0; r2 < 2; ++r2)
+        for (int g2 = 0; g2 < C::kGroups; ++g2) {
+          float s0, s1;                            // rows q and q + 8
+          uint32_t z0 = 0x43084308u, z1 = z0;      // bf16x2 of 128 + zero
+          if constexpr (kZeros) {
+            s0 = __uint_as_float(mv[2 * g2] << 16);
+            s1 = __uint_as_float(mv[2 * g2 + 1] << 16);
+            z0 = __byte_perm(mv[2 * g2], 0, 0x3232);
+            z1 = __byte_perm(mv[2 * g2 + 1], 0, 0x3232);
+          } else {
+            s0 = __uint_as_float(mv[g2] << 16);
+            s1 = __uint_as_float(mv[g2] & 0xffff0000u);
+          }
+          constexpr int kWords = 4 / C::kGroups;
+          uint32_t f[kWords][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              w[r2][h] = *reinterpret_cast<const uint4*>(st + (i * 4 + r2 * 2 + h) * 512 + lane * 16);
+          for (int jj = 0; jj < kWords; ++jj)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 lo = w[0][j >> 1], hi = w[1][j >> 1];
-            const uint32_t f[4] = {(j & 1) ? lo.z : lo.x, (j & 1) ? hi.z : hi.x, (j & 1) ? lo.w : lo.y,
-                                   (j & 1) ? hi.w : hi.y};
+            for (int n = 0; n < 4; ++n)
+              f[jj][n] = sub_bf16x2(((w[2 * g2 + jj] >> (4 * n)) & 0x000f000fu) | 0x43004300u, (n & 1) ? z1 : z0);
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) {
+          for (int n = 0; n < kNT; ++n) {
+            if (n == 1 && !both) break;
+            float part[4] = {};
+#pragma unroll
+            for (int jj = 0; jj < kWords; ++jj) {
+              const int j = 2 * g2 + jj;
               const uint4 v = x[n][j >> 1];
-              if (j & 1) mma_bf16(acc[i][n], f, v.z, v.w);
-              else mma_bf16(acc[i][n], f, v.x, v.y);
+              if (j & 1) mma_bf16(part, f[jj], v.z, v.w);
+              else mma_bf16(part, f[jj], v.x, v.y);
             }
+            acc[i][n][0] += s0 * part[0];
+            acc[i][n][1] += s0 * part[1];
+            acc[i][n][2] += s1 * part[2];
+            acc[i][n][3] += s1 * part[3];
+          }
+        }
+      } else {
+        uint4 w[2][2];  // rows q, q + 8; halves of the block
+#pragma unroll
+        for (int r2 = 0; r2 < 2; ++r2)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            w[r2][h] = *reinterpret_cast<const uint4*>(st + (i * 4 + r2 * 2 + h) * 512 + lane * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 lo = w[0][j >> 1], hi = w[1][j >> 1];
+          const uint32_t f[4] = {(j & 1) ? lo.z : lo.x, (j & 1) ? hi.z : hi.x, (j & 1) ? lo.w : lo.y,
+                                 (j & 1) ? hi.w : hi.y};
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            const uint4 v = x[n][j >> 1];
+            if (j & 1) mma_bf16(acc[i][n], f, v.z, v.w);
+            else mma_bf16(acc[i][n], f, v.x, v.y);
           }
         }
       }
+    }
+  };
+
+  uint4 xa[kNT][2], xb[kNT][2];
+  aim_x();
+  load_x(xa);
+#pragma unroll 1
+  for (int u = blockIdx.x + group * gridDim.x; u < units; u += stride) {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+#pragma unroll
+        for (int i = 0; i < C::kMats; ++i) acc[i][n][v] = 0.f;
+        tot[n][v] = 0.f;
+      }
+    while (cur.n && cur.u == u) {
+      members = tokens_of(cur.ent);
+      if constexpr (kNT == 2 && kKind != kMvOne) {
+        tile0 = (members & 0xffu) == 0 ? 1 : 0;
+        both = (members & 0xffu) != 0 && members > 0xffu;
+      }
+      int n = cur.n;
+#pragma unroll 1
+      for (; n >= 2; n -= 2) {
+        block(xa, xb);
+        block(xb, xa);
+      }
+      if (n) {
+        block(xa, xb);
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) {
+          xa[i][0] = xb[i][0];
+          xa[i][1] = xb[i][1];
+        }
+      }
       const int ent = cur.ent;
-      advance(cur);
-      if (kKind == kMvDown && (cur.u != u || cur.ent != ent)) close_entry(ent);
+      next_segment(cur);
+      if constexpr (kKind == kMvDown) {
+        // the router weights of the matrix that ends here
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+          for (int t2 = 0; t2 < 2; ++t2) {
+            const int t = 8 * (tile0 + n) + 2 * c + t2;
+            if (t < 8 * kNT && (members >> t & 1)) {
+              const float w = ent == nhit ? 1.f : hits->weight[hits->first[ent] + __popc(members & ((1u << t) - 1))];
+              const float y0 = w * acc[0][n][t2], y1 = w * acc[0][n][2 + t2];
+              if (kNT == 1 || n == 1 || tile0 == 0) {
+                tot[n][t2] += y0;
+                tot[n][2 + t2] += y1;
+              } else {
+                tot[kNT - 1][t2] += y0;
+                tot[kNT - 1][2 + t2] += y1;
+              }
+            }
+            acc[0][n][t2] = acc[0][n][2 + t2] = 0.f;
+          }
+        }
+      }
     }
 
-    // ---- the warps' sums meet ----
-    float* mine = red + (parity * kMvWarps + warp) * C::kRed;
-#pragma unroll
-    for (int i = 0; i < C::kMats; ++i)
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          mine[(i * C::kCols + 8 * n + 2 * c + (v & 1)) * C::kRedLd + q + 8 * (v >> 1)] =
-              kKind == kMvDown ? tot[n][v] : acc[i][n][v];
-    __syncthreads();
-    const int o = threadIdx.x;
-    if (o < kMvRows * C::kCols) {
-      const int r = o % kMvRows, t = o / kMvRows;
-      float s[C::kMats];
-#pragma unroll
-      for (int i = 0; i < C::kMats; ++i) {
-        s[i] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kMvWarps; ++w)
-          s[i] += red[(parity * kMvWarps + w) * C::kRed + (i * C::kCols + t) * C::kRedLd + r];
-      }
+    // ---- the result: straight from the fragments, or where the group's sums meet ----
+    auto emit = [&](int t, int r, float s0, float s1) {
       int tile = u, R = a.m.R;
       int64_t row = t;
       bool in = t < a.T;
       if constexpr (kKind == kMvUp) {
-        const bool sh = u >= nhit * tiles;
-        tile = sh ? u - nhit * tiles : u % tiles;
-        if (sh) {
+        if (u >= routed) {
+          tile = u - routed;
           R = a.shared.R;
-          row = (int64_t)a.T * a.k + t;
+          row = a.T * a.k + t;
         } else {
-          const int ent = u / tiles, e = hits->expert[ent];
-          in = in && (hits->mask[ent] >> t & 1);
-          int j = 0;
-          if (in)
-            while (j < a.k - 1 && hits->id[t * a.k + j] != e) ++j;
-          row = (int64_t)t * a.k + j;
+          const int ent = u / tiles;
+          const uint32_t m = hits->mask[ent];
+          tile = u - ent * tiles;
+          in = m >> t & 1;
+          row = hits->first[ent] + __popc(m & ((1u << t) - 1));
         }
       }
       const int col = tile * kMvRows + r;
-      if (in && col < R) {
-        const int64_t at = row * a.ldo + col;
-        float v = s[0];
-        if constexpr (kDual) {
-          v = swiglu(s[0], s[1]);
-          if (kKind == kMvOne && a.u) {
-            a.u[at] = (uint16_t)(pack_bf16x2(s[0], 0.f) & 0xffffu);
-            a.g[at] = (uint16_t)(pack_bf16x2(s[1], 0.f) & 0xffffu);
-          }
+      if (!in || col >= R) return;
+      const int64_t at = row * a.ldo + col;
+      float v = s0;
+      if constexpr (kDual) {
+        v = swiglu(s0, s1);
+        if (kKind == kMvOne && a.u) {
+          a.u[at] = (uint16_t)(pack_bf16x2(s0, 0.f) & 0xffffu);
+          a.g[at] = (uint16_t)(pack_bf16x2(s1, 0.f) & 0xffffu);
         }
-        if (a.out_bf16) static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
-        else static_cast<float*>(a.out)[at] = v;
+      }
+      if (a.out_bf16) static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
+      else static_cast<float*>(a.out)[at] = v;
+    };
+    float* mine = red + warp * C::kRed;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      // an expert with tokens in the second tile only has its sums in the first place
+      const int at = kKind == kMvUp && kNT == 2 ? (n + tile0) & 1 : n;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int t = 8 * at + 2 * c + (v & 1), r = q + 8 * (v >> 1);
+        const float s0 = kKind == kMvDown ? tot[n][v] : acc[0][n][v];
+        if (wk == 1) {
+          emit(t, r, s0, acc[C::kMats - 1][n][v]);
+        } else {
+          mine[red_at(t, r)] = s0;
+          if constexpr (kDual) mine[C::kCols * kMvRows + red_at(t, r)] = acc[1][n][v];
+        }
       }
     }
-    parity ^= 1;  // the next unit writes the other buffer: one barrier a unit is enough
+    if (wk > 1) {
+      named_bar_sync(1 + group, wk * 32);
+      for (int o = part * 32 + lane; o < kMvRows * C::kCols; o += wk * 32) {
+        const int r = o % kMvRows, t = o / kMvRows;
+        const float* p = red + group * wk * C::kRed + red_at(t, r);
+        float s0 = 0.f, s1 = 0.f;
+        for (int w = 0; w < wk; ++w) {  // in warp order
+          s0 += p[w * C::kRed];
+          if constexpr (kDual) s1 += p[w * C::kRed + C::kCols * kMvRows];
+        }
+        emit(t, r, s0, s1);
+      }
+      named_bar_sync(1 + group, wk * 32);  // before the next unit's sums
+    }
   }
   cp_async_wait<0>();
 }
@@ -466,9 +561,9 @@ template <bool kW4, bool kDual, int kKind, int kNT, bool kG32, bool kZeros>
 cudaError_t launch_mv(const MvArgs& a, int64_t units, int num_sms, cudaStream_t stream) {
   using C = Mv<kW4, kDual, kKind, kNT, kG32, kZeros>;
   auto* k = mv_kernel<kW4, kDual, kKind, kNT, kG32, kZeros>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(units, C::kPerSm * num_sms));
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(units, num_sms));
   return launch_k(k, dim3(grid), dim3(kMvThreads), C::kSmem, stream, a);
 }
 
@@ -510,10 +605,9 @@ __device__ __forceinline__ void store_codes(uint8_t* codes, int64_t tile, int nb
   }
 }
 
-__device__ __forceinline__ void store_scale(uint8_t* scales, int64_t tile, int G, int g, int row, bool zeros, uint32_t s,
-                                            uint32_t zero) {
-  const int at = 2 * (row & 7) + (row >> 3);
-  const int64_t o = (tile * G + g) * kMvRows + at;
+__device__ __forceinline__ void store_scale(uint8_t* scales, int64_t tile, int stored, int group, int g, int row, bool zeros,
+                                            uint32_t s, uint32_t zero) {
+  const int64_t o = tile * stored * kMvRows + int4_scale_at(row, g, group);
   if (zeros)
     reinterpret_cast<uint32_t*>(scales)[o] = s | (pack_bf16x2(128.f + (float)zero, 0.f) << 16);
   else
@@ -529,7 +623,8 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const uint16_t* __re
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, q = lane >> 2, c = lane & 3;
-  const int nb = (int)int4_col_blocks(K), np = (nb + 1) / 2, G = (int)int4_groups(K, group);
+  const int nb = (int)int4_col_blocks(K), np = (nb + 1) / 2;
+  const int stored = (int)int4_stored_groups(K, group);
   const int64_t tiles = int4_row_tiles(R), items = tiles * np;
   for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * 8) {
     const int64_t tile = it / np;
@@ -582,7 +677,7 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const uint16_t* __re
           v[p >> 1][p & 1][r][i] =
               s > 0.f ? (uint8_t)fminf(fmaxf(rintf(__fdiv_rn(f[p >> 1][p & 1][r][i], s)) + zero, 0.f), 15.f) : (uint8_t)8;
         const int g = (kb0 * kMvBK + 32 * p) / group;
-        if (p == first && c == 0 && g < G) store_scale(scales, tile, G, g, q + 8 * r, kZeros, sb, (uint32_t)zero);
+        if (p == first && c == 0 && g < stored) store_scale(scales, tile, stored, group, g, q + 8 * r, kZeros, sb, (uint32_t)zero);
       }
     store_codes(codes, tile, nb, kb0, v);
   }
@@ -595,6 +690,7 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const uint8_t* __restric
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, q = lane >> 2, c = lane & 3;
   const int nb = (int)int4_col_blocks(K), np = (nb + 1) / 2, G = (int)int4_groups(K, group);
+  const int stored = (int)int4_stored_groups(K, group);
   const int64_t tiles = int4_row_tiles(R), items = tiles * np;
   for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * 8) {
     const int64_t tile = it / np;
@@ -611,9 +707,9 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const uint8_t* __restric
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[p >> 1][p & 1][r][i] = (uint8_t)(x >> (4 * i) & 15u);
         const int g = (kb0 * kMvBK + 32 * p) / group;
-        if ((kb0 * kMvBK + 32 * p) % group == 0 && c == 0 && g < G) {
-          const bool in = row < R;
-          store_scale(scales, tile, G, g, q + 8 * r, z != nullptr, in ? __ldg(s + row * G + g) : 0u,
+        if ((kb0 * kMvBK + 32 * p) % group == 0 && c == 0 && g < stored) {
+          const bool in = row < R && g < G;
+          store_scale(scales, tile, stored, group, g, q + 8 * r, z != nullptr, in ? __ldg(s + row * G + g) : 0u,
                       in && z ? __ldg(z + row * G + g) : 8u);
         }
       }

@@ -21,16 +21,26 @@ constexpr int kMvMaxSlots = kMvTokens * kMaxTopK;
 // k = 32 h + 8 c + 4 i + {0, 1, 2, 3}: bits 4 n .. 4 n + 3 for n = 0..7 are
 //   (q, k), (q + 8, k), (q, k + 2), (q + 8, k + 2), (q, k + 1), (q + 8, k + 1), (q, k + 3), (q + 8, k + 3)
 // so that one mask of both half words gives two neighbouring columns of a row.
-// Scales: per row tile and group, 16 entries in the order q = 0, 8, 1, 9, ...: an entry is the bf16
-// scale, or, with zero points, the scale (low half word) and bf16(128 + zero) (high half word).
+// Scales: per row tile, then per K block (group 32 or 64) or pair of K blocks (128), then per q = 0..7,
+// then (group 32) per half of the block, the entries of rows q and q + 8, so that one copy brings a
+// lane all it needs. An entry is the bf16 scale, or, with zero points, the scale (low half word) and
+// bf16(128 + zero) (high half word). Groups past the last column have entries too.
 __host__ __device__ inline int64_t int4_row_tiles(int64_t rows) { return (rows + kMvRows - 1) / kMvRows; }
 __host__ __device__ inline int64_t int4_col_blocks(int64_t cols) { return (cols + kMvBK - 1) / kMvBK; }
 __host__ __device__ inline int64_t int4_groups(int64_t cols, int group) { return (cols + group - 1) / group; }
 __host__ __device__ inline int64_t int4_code_bytes(int64_t rows, int64_t cols) {
   return int4_row_tiles(rows) * int4_col_blocks(cols) * 512;
 }
+// entries of a row in the library's layout: whole blocks of 64 columns (groups of 32 come in pairs)
+__host__ __device__ inline int64_t int4_stored_groups(int64_t cols, int group) {
+  return group == 32 ? 2 * int4_col_blocks(cols) : int4_groups(cols, group);
+}
 __host__ __device__ inline int64_t int4_scale_bytes(int64_t rows, int64_t cols, int group, bool zeros) {
-  return int4_row_tiles(rows) * int4_groups(cols, group) * kMvRows * (zeros ? 4 : 2);
+  return int4_row_tiles(rows) * int4_stored_groups(cols, group) * kMvRows * (zeros ? 4 : 2);
+}
+// Entry of (row r of the tile, group g) among a tile's.
+__host__ __device__ inline int int4_scale_at(int r, int g, int group) {
+  return group == 32 ? (g >> 1) * 32 + (r & 7) * 4 + (g & 1) * 2 + (r >> 3) : g * 16 + (r & 7) * 2 + (r >> 3);
 }
 
 // One or two matrices of equal shape (two: up and gate), bf16 [R][K] or 4-bit.
@@ -64,8 +74,8 @@ struct MvArgs {
 // kind: what a unit of 16 rows is
 enum MvKind : int {
   kMvOne = 0,      // one matrix (dual: a pair): out[t] = W x_t (dual: SwiGLU)
-  kMvUp = 1,       // dual, per expert hit: h of every slot (t, first j with that expert), and of the
-                   // shared expert at rows T * k + t
+  kMvUp = 1,       // dual, per expert hit: h of its tokens, a row each (experts and tokens in rising
+                   // order), and of the shared expert at rows T * k + t
   kMvDown = 2,     // sum over the experts hit (and the shared one): out[t] = sum w W_down h
 };
 

@@ -58,11 +58,14 @@ def _unpack(m):
                     for n, (dr, dk) in enumerate(where):
                         code[:, i + dr, :, 32 * h + 8 * j + 4 * mm + dk] = w[:, :, i, j, h, mm] >> (4 * n) & 15
     code = code.reshape(-1, nb * 64)
-    order = [r for p in range(8) for r in (p, p + 8)]
-    e = m.scales.cpu().numpy().view(np.uint32 if m.zeros else np.uint16).reshape(-1, G, 16)
-    rows = np.empty_like(e)
-    rows[:, :, order] = e
-    rows = rows.transpose(0, 2, 1).reshape(-1, G)
+    N = 2 * nb if m.group == 32 else G
+    e = m.scales.cpu().numpy().view(np.uint32 if m.zeros else np.uint16).reshape(-1, 16 * N)
+    r, g = np.arange(16)[:, None], np.arange(G)[None, :]
+    if m.group == 32:
+        at = 32 * (g // 2) + 4 * (r % 8) + 2 * (g % 2) + r // 8
+    else:
+        at = 16 * g + 2 * (r % 8) + r // 8
+    rows = e[:, at].reshape(-1, G)
     zero = None
     if m.zeros:
         zero = torch.from_numpy((rows >> 16).astype(np.uint16).view(np.int16)).view(torch.bfloat16).float().numpy() - 128
