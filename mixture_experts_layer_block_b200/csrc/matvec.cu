@@ -97,6 +97,89 @@ struct Walk {
   int kb;     // block of the matrix where the segment begins
 };
 
+// Scratch bytes of build_hits: a word per expert, the chunks' totals, the batch's ids and weights.
+constexpr int hit_scratch(int slots) { return (kMaxExperts + 32 + 2 * slots) * 4; }
+
+// Every thread of the CTA: the hit list of the batch. Integers only, and weights added in slot order.
+__device__ __forceinline__ void build_hits(const MvArgs& a, Hits* hits, uint32_t* scratch) {
+  uint32_t* emask = scratch;  // tokens by expert; later | index in the hit list << 16
+  int* chunk = reinterpret_cast<int*>(scratch + kMaxExperts);  // experts hit | pairs << 16, of 32 experts
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = a.T * a.k, s = threadIdx.x;
+  int* ids = chunk + 32;
+  float* w = reinterpret_cast<float*>(ids + S);
+  static_assert(kMvThreads >= kMvMaxSlots && kMvWarps * 64 >= kMaxExperts, "a thread per slot, two chunks a warp");
+  int e = -1;
+  if (s < S) {
+    e = __ldcg(a.ids + s);
+    w[s] = __ldcg(a.topk_w + s);
+    ids[s] = e;
+  }
+  for (int i = threadIdx.x; i < a.E; i += kMvThreads) emask[i] = 0;
+  __syncthreads();
+  const bool in = e >= 0 && e < a.E;
+  const int t = s / a.k;
+  if (in) atomicOr(&emask[e], 1u << t);
+  __syncthreads();
+  // chunks of 32 experts: warp w's are w and w + 16
+  const int chunks = (a.E + 31) >> 5;
+  uint32_t m[2], any[2];
+  int sum[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int x = (warp + kMvWarps * i) * 32 + lane;
+    m[i] = x < a.E ? emask[x] : 0;
+    if (a.capacity > 0)
+      while (__popc(m[i]) > a.capacity) m[i] &= ~(0x80000000u >> __clz(m[i]));  // the highest token is dropped
+    any[i] = __ballot_sync(0xffffffffu, m[i] != 0);
+    sum[i] = __popc(m[i]);  // inclusive scan of the pairs
+    if (any[i]) {
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, sum[i], o);
+        if (lane >= o) sum[i] += v;
+      }
+    }
+    if (lane == 31) chunk[warp + kMvWarps * i] = __popc(any[i]) | sum[i] << 16;
+  }
+  __syncthreads();
+  int before = lane < chunks ? chunk[lane] : 0;  // both counts at once: neither reaches 2^15
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (threadIdx.x == 31) hits->n = before & 0xffff;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int ch = warp + kMvWarps * i, x = ch * 32 + lane;
+    const int base = __shfl_sync(0xffffffffu, before, ch == 0 ? 0 : ch - 1);
+    if (m[i]) {
+      const int at = (ch ? base & 0xffff : 0) + __popc(any[i] & ((1u << lane) - 1));
+      hits->expert[at] = (uint16_t)x;
+      hits->mask[at] = (uint16_t)m[i];
+      hits->first[at] = (uint16_t)((ch ? base >> 16 : 0) + sum[i] - __popc(m[i]));
+    }
+    if (x < a.E) emask[x] = m[i] ? m[i] | (uint32_t)((ch ? base & 0xffff : 0) + __popc(any[i] & ((1u << lane) - 1))) << 16 : 0;
+  }
+  __syncthreads();
+  if (in) {
+    const uint32_t v = emask[e], mask = v & 0xffffu;
+    float weight = 0.f;
+    bool first = mask >> t & 1;
+    for (int j = t * a.k; j < (t + 1) * a.k; ++j)
+      if (ids[j] == e) {
+        if (j < s) first = false;
+        weight += w[j];
+      }
+    if (first) hits->weight[hits->first[v >> 16] + __popc(mask & ((1u << t) - 1))] = weight;
+  }
+  __syncthreads();
+}
+
+// What lanes without a token read in place of its activations.
+__device__ const uint4 kMvZeros[8] = {};
+
 // A sum's place in a warp's partial sums: 16 rows to a token, rotated so that the four tokens that a
 // quarter warp writes at once fall into different banks.
 __device__ __forceinline__ int red_at(int col, int row) { return col * kMvRows + ((row + 4 * (col >> 1)) & 15); }
@@ -106,7 +189,6 @@ __device__ __forceinline__ int red_at(int col, int row) { return col * kMvRows +
 template <bool kW4, bool kDual, int kKind, int kNT, bool kG32, bool kZeros>
 __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant__ MvArgs a) {
   using C = Mv<kW4, kDual, kKind, kNT, kG32, kZeros>;
-  constexpr int kThreads = kMvThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = lane >> 2, c = lane & 3;
@@ -118,57 +200,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   if (!a.early) griddep_wait();
   int nhit = 1;
   if constexpr (kKind != kMvOne) {
-    // the partial sums' buffer is free until the first unit: the experts' token masks
-    uint32_t* emask = reinterpret_cast<uint32_t*>(red);
-    static_assert(kMvWarps * C::kRed * 4 >= kMaxExperts * 4, "the masks fit");
-    for (int e = threadIdx.x; e < a.E; e += kThreads) emask[e] = 0;
-    __syncthreads();
-    for (int s = threadIdx.x; s < a.T * a.k; s += kThreads) {
-      const int e = __ldcg(a.ids + s);
-      if (e >= 0 && e < a.E) atomicOr(&emask[e], 1u << (s / a.k));
-    }
-    __syncthreads();
-    if (warp == 0) {
-      int n = 0, pairs = 0;
-      for (int e0 = 0; e0 < a.E; e0 += 32) {
-        uint32_t m = e0 + lane < a.E ? emask[e0 + lane] : 0;
-        if (a.capacity > 0)
-          while (__popc(m) > a.capacity) m &= ~(0x80000000u >> __clz(m));  // the highest token is dropped
-        const uint32_t any = __ballot_sync(0xffffffffu, m != 0);
-        if (any == 0) continue;
-        int sum = __popc(m);  // inclusive scan of the pairs
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const int v = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += v;
-        }
-        if (m) {
-          const int at = n + __popc(any & ((1u << lane) - 1));
-          hits->expert[at] = (uint16_t)(e0 + lane);
-          hits->mask[at] = (uint16_t)m;
-          hits->first[at] = (uint16_t)(pairs + sum - __popc(m));
-        }
-        n += __popc(any);
-        pairs += __shfl_sync(0xffffffffu, sum, 31);
-      }
-      if (lane == 0) hits->n = n;
-    }
-    __syncthreads();
+    build_hits(a, hits, reinterpret_cast<uint32_t*>(red));  // the sums' buffer is free until the first unit
+    static_assert(kMvWarps * C::kRed * 4 >= hit_scratch(kNT * 8 * kMaxTopK), "its scratch memory fits");
     nhit = hits->n;
-    if constexpr (kKind == kMvDown) {
-      for (int i = threadIdx.x; i < nhit; i += kThreads) {
-        const int e = hits->expert[i];
-        int pair = hits->first[i];
-        for (uint32_t m = hits->mask[i]; m; m &= m - 1) {
-          const int t = __ffs(m) - 1;
-          float w = 0.f;
-          for (int j = 0; j < a.k; ++j)
-            if (__ldcg(a.ids + t * a.k + j) == e) w += __ldcg(a.topk_w + t * a.k + j);
-          hits->weight[pair++] = w;
-        }
-      }
-      __syncthreads();
-    }
   }
 
   const int tiles = ceil_div(a.m.R, kMvRows), nb = ceil_div(a.m.K, kMvBK);
@@ -176,9 +210,21 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   const int routed = kKind == kMvUp ? nhit * tiles : tiles;  // units of the routed experts
   const int units = kKind == kMvUp ? routed + stiles : tiles;
 
-  // `wk` warps share a unit: as many as keep every warp busy
-  int wk = kMvWarps;
-  while (wk > 1 && (int64_t)units * wk > (int64_t)gridDim.x * kMvWarps) wk >>= 1;
+  // `wk` warps share a unit: the number that ends the whole work first
+  // (in blocks of K: a round of units takes each warp its share, and about 3 for the unit's end)
+  int wk = 1;
+  {
+    const int len = kKind == kMvDown ? nhit * nb + snb : nb;
+    int64_t best = INT64_MAX;
+    for (int w = kMvWarps; w >= 1; w >>= 1) {
+      const int64_t rounds = ((int64_t)units * w + gridDim.x * kMvWarps - 1) / (gridDim.x * kMvWarps);
+      const int64_t cost = rounds * ((len + w - 1) / w + 3);
+      if (cost < best) {
+        best = cost;
+        wk = w;
+      }
+    }
+  }
   const int group = warp / wk, part = warp - group * wk;  // groups of warps take units in turn
   const int stride = gridDim.x * (kMvWarps / wk);
 
@@ -285,8 +331,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   // tiles, only that one is computed: `tile0` is the first tile with a token, `both` whether the
   // other one has some too.
   Walk nxt{};
-  const uint16_t* xp[kNT];       // null: not a token of this expert
+  const uint16_t* xp[kNT];       // zeros where the lane has no token of this expert
+  int xstep[kNT];                // elements to the next block (0: zeros)
   int xk = 0;                    // columns from this lane's first one to the end
+  int xtiles = kNT;              // token tiles to load
   auto tokens_of = [&](int ent) -> uint32_t {
     return kKind == kMvOne || ent == nhit ? (1u << a.T) - 1 : hits->mask[ent];
   };
@@ -303,18 +351,29 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       int64_t row = t;
       if constexpr (kKind == kMvDown)  // h's rows
         row = sh ? a.T * a.k + t : hits->first[nxt.ent] + __popc(members & ((1u << t) - 1));
-      xp[n] = t < 8 * kNT && (members >> t & 1) ? a.x + row * a.ldx + col : nullptr;
+      const bool in = t < 8 * kNT && (members >> t & 1);
+      xp[n] = in ? a.x + row * a.ldx + col : reinterpret_cast<const uint16_t*>(kMvZeros);
+      xstep[n] = in ? kMvBK : 0;
     }
+    if constexpr (kNT == 2 && kKind != kMvOne) xtiles = (members & 0xffu) != 0 && members > 0xffu ? 2 : 1;
   };
   auto load_x = [&](uint4 (&x)[kNT][2]) {  // the next block's, if there is one
     if (nxt.n == 0) return;
+    // plain loads: the warps of an SM share the rows through L1
+    if (xk + 8 * c >= kMvBK) {  // the block is whole (the same for every lane)
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      const bool in = xp[n] != nullptr;
-      // plain loads: the warps of an SM share the rows through L1
-      x[n][0] = in && xk > 0 ? *reinterpret_cast<const uint4*>(xp[n]) : make_uint4(0, 0, 0, 0);
-      x[n][1] = in && xk > 32 ? *reinterpret_cast<const uint4*>(xp[n] + 32) : make_uint4(0, 0, 0, 0);
-      if (in) xp[n] += kMvBK;
+      for (int n = 0; n < kNT; ++n) {
+        if (n >= xtiles) break;
+        x[n][0] = *reinterpret_cast<const uint4*>(xp[n]);
+        x[n][1] = *reinterpret_cast<const uint4*>(xp[n] + 32);
+        xp[n] += xstep[n];
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        x[n][0] = xk > 0 ? *reinterpret_cast<const uint4*>(xp[n]) : make_uint4(0, 0, 0, 0);
+        x[n][1] = xk > 32 ? *reinterpret_cast<const uint4*>(xp[n] + 32) : make_uint4(0, 0, 0, 0);
+      }
     }
     xk -= kMvBK;
     if (--nxt.n == 0) {
