@@ -3,8 +3,9 @@
 // What bounds them: the weights' bytes, each read once from HBM, and at the smallest sizes the
 // latency of one trip there. So the design is about bytes in flight and short dependent chains:
 //  - a unit is 16 output rows (for the experts: of one expert, or, in the down projection, of the sum
-//    over all experts that were hit); 1 to 16 warps split its K blocks evenly, as many as keep all
-//    warps of the GPU busy, and the down projection's K runs over every expert hit;
+//    over all experts that were hit, whose K blocks then follow one another). A CTA (one to an SM) has
+//    a run of units, and its 16 warps split the run's K blocks evenly, whatever the units' number and
+//    length;
 //  - each lane copies its own 16-byte pieces of weights to shared memory with cp.async, a fixed number
 //    of blocks ahead and across unit boundaries, and reads only its own: no barrier in the K loop;
 //  - the products run on mma.sync m16n8k16 (fp32 accumulation): weights come out of a register
@@ -13,8 +14,8 @@
 //  - 4-bit codes become bf16 exactly: (code | 0x4300) is 128 + code, less bf16(128 + zero). A group's
 //    sum is scaled in fp32, so nothing is rounded before the result;
 //  - a kernel behind another of the same call starts copying weights before that one is done.
-// Partial sums of one unit meet in shared memory and are added in warp order: equal inputs give equal
-// bits.
+// The sums of a unit that several warps share meet in shared memory and are added in warp order: equal
+// inputs give equal bits.
 #include <algorithm>
 
 #include "ffn.cuh"
@@ -86,13 +87,12 @@ struct Mv {
   static_assert(kDepth >= 3, "two blocks in flight beside the one in use");
 };
 
-// Where a warp is in its sequence of K blocks: units of 16 output rows, in each a share of the unit's K
-// blocks, which run over one matrix or (kMvDown) over those of all experts hit. A segment is a run of
-// blocks of one matrix.
+// Where a warp is in its share of the CTA's K blocks. A segment is a run of blocks of one matrix within
+// one unit.
 struct Walk {
   int u;      // unit
-  int left;   // blocks of this unit's share behind this segment
-  int n;      // blocks of this segment from here on (0 past the last unit)
+  int rest;   // blocks of the share behind this segment
+  int n;      // blocks of the segment from here on (0 past the share's end)
   int ent;    // the matrix: entry of the hit list (its length: the shared expert)
   int kb;     // block of the matrix where the segment begins
 };
@@ -210,60 +210,43 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   const int routed = kKind == kMvUp ? nhit * tiles : tiles;  // units of the routed experts
   const int units = kKind == kMvUp ? routed + stiles : tiles;
 
-  // `wk` warps share a unit: the number that ends the whole work first
-  // (in blocks of K: a round of units takes each warp its share, and about 3 for the unit's end)
-  int wk = 1;
-  {
-    const int len = kKind == kMvDown ? nhit * nb + snb : nb;
-    int64_t best = INT64_MAX;
-    for (int w = kMvWarps; w >= 1; w >>= 1) {
-      const int64_t rounds = ((int64_t)units * w + gridDim.x * kMvWarps - 1) / (gridDim.x * kMvWarps);
-      const int64_t cost = rounds * ((len + w - 1) / w + 3);
-      if (cost < best) {
-        best = cost;
-        wk = w;
-      }
-    }
-  }
-  const int group = warp / wk, part = warp - group * wk;  // groups of warps take units in turn
-  const int stride = gridDim.x * (kMvWarps / wk);
+  // This CTA's units, its K blocks one after another (each unit has as many), and this warp's even
+  // share of them: whole units, but for the first and the last.
+  const int u0 = (int)((int64_t)blockIdx.x * units / gridDim.x);
+  const int len = kKind == kMvDown ? nhit * nb + snb : nb;
+  const int total = ((int)((int64_t)(blockIdx.x + 1) * units / gridDim.x) - u0) * len;
+  auto share = [&](int w) { return (int)((int64_t)w * total / kMvWarps); };  // where warp w's begins
 
-  // The first segment of this warp's share of unit p.u, or of the next unit where it has one.
-  auto start_unit = [&](Walk& p) {
-    for (; p.u < units; p.u += stride) {
-      const bool sh = kKind == kMvUp && p.u >= routed;
-      const int total = kKind == kMvDown ? nhit * nb + snb : (sh ? snb : nb);
-      const int b = (int)((int64_t)part * total / wk), n = (int)((int64_t)(part + 1) * total / wk) - b;
-      if (n == 0) continue;  // fewer blocks than warps: nothing of this unit is this warp's
-      if constexpr (kKind == kMvDown) {
-        p.ent = min(b / nb, nhit);
-        p.kb = b - p.ent * nb;
-        p.n = min(n, (p.ent == nhit ? snb : nb) - p.kb);
-      } else {
-        p.ent = kKind == kMvUp ? (sh ? nhit : p.u / tiles) : 0;
-        p.kb = b;
-        p.n = n;
-      }
-      p.left = n - p.n;
-      return;
-    }
-    p.n = 0;
+  auto set_segment = [&](Walk& p, int left) {  // p.u, p.ent and p.kb are set; `left` blocks of the share
+    const int seg = (kKind != kMvOne && p.ent == nhit ? snb : nb) - p.kb;
+    p.n = min(left, seg);
+    p.rest = left - p.n;
   };
   auto next_segment = [&](Walk& p) {
-    if (kKind == kMvDown && p.left > 0) {
-      ++p.ent;
-      p.kb = 0;
-      p.n = min(p.left, p.ent == nhit ? snb : nb);
-      p.left -= p.n;
-    } else {
-      p.u += stride;
-      start_unit(p);
+    if (p.rest == 0) {
+      p.n = 0;
+      return;
     }
+    p.kb = 0;
+    if (kKind == kMvDown && p.ent + 1 < nhit + (snb ? 1 : 0)) {
+      ++p.ent;
+    } else {
+      ++p.u;
+      p.ent = kKind == kMvUp ? (p.u >= routed ? nhit : p.u / tiles) : 0;
+    }
+    set_segment(p, p.rest);
   };
 
   // ---- weights: this lane's pieces of a block, from running addresses ----
   Walk prod{};
-  prod.u = blockIdx.x + group * gridDim.x;
+  const int first = share(warp);
+  if (first < share(warp + 1)) {
+    const int b = first % len;
+    prod.u = u0 + first / len;
+    prod.ent = kKind == kMvDown ? min(b / nb, nhit) : (kKind == kMvUp ? (prod.u >= routed ? nhit : prod.u / tiles) : 0);
+    prod.kb = kKind == kMvDown ? b - prod.ent * nb : b;
+    set_segment(prod, share(warp + 1) - first);
+  }
   const uint8_t* wp[C::kMats];   // 4-bit: codes; bf16: row q
   const uint8_t* sp[C::kMats];   // 4-bit: scales; bf16: row q + 8
   bool in0 = true, in1 = true;   // bf16: rows q and q + 8 exist
@@ -382,7 +365,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     }
   };
 
-  start_unit(prod);
   Walk cur = prod;
   nxt = prod;
   aim_weights();
@@ -412,7 +394,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     const uint8_t* st = ring_p + slot;
     slot += C::kStage;
     if (slot == C::kStage * C::kDepth) slot = 0;
-    #pragma unroll
+#pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
         const uint4 w4 = *reinterpret_cast<const uint4*>(st + i * C::kMat + lane * 16);
@@ -491,8 +473,38 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   uint4 xa[kNT][2], xb[kNT][2];
   aim_x();
   load_x(xa);
-#pragma unroll 1
-  for (int u = blockIdx.x + group * gridDim.x; u < units; u += stride) {
+  auto emit = [&](int u, int t, int r, float s0, float s1) {  // output row r of unit u, token t
+    int tile = u, R = a.m.R;
+    int64_t row = t;
+    bool in = t < a.T;
+    if constexpr (kKind == kMvUp) {
+      if (u >= routed) {
+        tile = u - routed;
+        R = a.shared.R;
+        row = a.T * a.k + t;
+      } else {
+        const int ent = u / tiles;
+        const uint32_t m = hits->mask[ent];
+        tile = u - ent * tiles;
+        in = m >> t & 1;
+        row = hits->first[ent] + __popc(m & ((1u << t) - 1));
+      }
+    }
+    const int col = tile * kMvRows + r;
+    if (!in || col >= R) return;
+    const int64_t at = row * a.ldo + col;
+    float v = s0;
+    if constexpr (kDual) {
+      v = swiglu(s0, s1);
+      if (kKind == kMvOne && a.u) {
+        a.u[at] = (uint16_t)(pack_bf16x2(s0, 0.f) & 0xffffu);
+        a.g[at] = (uint16_t)(pack_bf16x2(s1, 0.f) & 0xffffu);
+      }
+    }
+    if (a.out_bf16) static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
+    else static_cast<float*>(a.out)[at] = v;
+  };
+  auto clear = [&]() {
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -501,117 +513,118 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
         for (int i = 0; i < C::kMats; ++i) acc[i][n][v] = 0.f;
         tot[n][v] = 0.f;
       }
-    while (cur.n && cur.u == u) {
-      members = tokens_of(cur.ent);
-      if constexpr (kNT == 2 && kKind != kMvOne) {
-        tile0 = (members & 0xffu) == 0 ? 1 : 0;
-        both = (members & 0xffu) != 0 && members > 0xffu;
-      }
-      int n = cur.n;
-#pragma unroll 1
-      for (; n >= 2; n -= 2) {
-        block(xa, xb);
-        block(xb, xa);
-      }
-      if (n) {
-        block(xa, xb);
-#pragma unroll
-        for (int i = 0; i < kNT; ++i) {
-          xa[i][0] = xb[i][0];
-          xa[i][1] = xb[i][1];
-        }
-      }
-      const int ent = cur.ent;
-      next_segment(cur);
-      if constexpr (kKind == kMvDown) {
-        // the router weights of the matrix that ends here
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-#pragma unroll
-          for (int t2 = 0; t2 < 2; ++t2) {
-            const int t = 8 * (tile0 + n) + 2 * c + t2;
-            if (t < 8 * kNT && (members >> t & 1)) {
-              const float w = ent == nhit ? 1.f : hits->weight[hits->first[ent] + __popc(members & ((1u << t) - 1))];
-              const float y0 = w * acc[0][n][t2], y1 = w * acc[0][n][2 + t2];
-              if (kNT == 1 || n == 1 || tile0 == 0) {
-                tot[n][t2] += y0;
-                tot[n][2 + t2] += y1;
-              } else {
-                tot[kNT - 1][t2] += y0;
-                tot[kNT - 1][2 + t2] += y1;
-              }
-            }
-            acc[0][n][t2] = acc[0][n][2 + t2] = 0.f;
-          }
-        }
-      }
-    }
-
-    // ---- the result: straight from the fragments, or where the group's sums meet ----
-    auto emit = [&](int t, int r, float s0, float s1) {
-      int tile = u, R = a.m.R;
-      int64_t row = t;
-      bool in = t < a.T;
-      if constexpr (kKind == kMvUp) {
-        if (u >= routed) {
-          tile = u - routed;
-          R = a.shared.R;
-          row = a.T * a.k + t;
-        } else {
-          const int ent = u / tiles;
-          const uint32_t m = hits->mask[ent];
-          tile = u - ent * tiles;
-          in = m >> t & 1;
-          row = hits->first[ent] + __popc(m & ((1u << t) - 1));
-        }
-      }
-      const int col = tile * kMvRows + r;
-      if (!in || col >= R) return;
-      const int64_t at = row * a.ldo + col;
-      float v = s0;
-      if constexpr (kDual) {
-        v = swiglu(s0, s1);
-        if (kKind == kMvOne && a.u) {
-          a.u[at] = (uint16_t)(pack_bf16x2(s0, 0.f) & 0xffffu);
-          a.g[at] = (uint16_t)(pack_bf16x2(s1, 0.f) & 0xffffu);
-        }
-      }
-      if (a.out_bf16) static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
-      else static_cast<float*>(a.out)[at] = v;
-    };
-    float* mine = red + warp * C::kRed;
+  };
+  // Calls f(token, row, sum, second matrix's sum) for this lane's sums of the unit.
+  auto each_sum = [&](auto&& f) {
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       // an expert with tokens in the second tile only has its sums in the first place
       const int at = kKind == kMvUp && kNT == 2 ? (n + tile0) & 1 : n;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int t = 8 * at + 2 * c + (v & 1), r = q + 8 * (v >> 1);
-        const float s0 = kKind == kMvDown ? tot[n][v] : acc[0][n][v];
-        if (wk == 1) {
-          emit(t, r, s0, acc[C::kMats - 1][n][v]);
-        } else {
-          mine[red_at(t, r)] = s0;
-          if constexpr (kDual) mine[C::kCols * kMvRows + red_at(t, r)] = acc[1][n][v];
+      for (int v = 0; v < 4; ++v)
+        f(8 * at + 2 * c + (v & 1), q + 8 * (v >> 1), kKind == kMvDown ? tot[n][v] : acc[0][n][v], acc[C::kMats - 1][n][v]);
+    }
+  };
+  auto put = [&](float* dst) {
+    each_sum([&](int t, int r, float s0, float s1) {
+      dst[red_at(t, r)] = s0;
+      if constexpr (kDual) dst[C::kCols * kMvRows + red_at(t, r)] = s1;
+    });
+  };
+
+  // Units that this warp computes whole go straight to memory. Of a unit that begins in another
+  // warp's share the sums go to `red`; those of one that ends in another's stay in registers until
+  // every warp is done with the ring, and go there.
+  bool open = false;  // the registers hold the beginning of a unit that another warp ends
+  bool mid = first % max(len, 1) != 0;
+  clear();
+#pragma unroll 1
+  while (cur.n) {
+    members = tokens_of(cur.ent);
+    if constexpr (kNT == 2 && kKind != kMvOne) {
+      tile0 = (members & 0xffu) == 0 ? 1 : 0;
+      both = (members & 0xffu) != 0 && members > 0xffu;
+    }
+    int n = cur.n;
+#pragma unroll 1
+    for (; n >= 2; n -= 2) {
+      block(xa, xb);
+      block(xb, xa);
+    }
+    if (n) {
+      block(xa, xb);
+#pragma unroll
+      for (int i = 0; i < kNT; ++i) {
+        xa[i][0] = xb[i][0];
+        xa[i][1] = xb[i][1];
+      }
+    }
+    const int ent = cur.ent;
+    const int u = cur.u;
+    next_segment(cur);
+    if constexpr (kKind == kMvDown) {
+      // the router weights of the matrix that ends here
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {
+          const int t = 8 * (tile0 + n) + 2 * c + t2;
+          if (t < 8 * kNT && (members >> t & 1)) {
+            const float w = ent == nhit ? 1.f : hits->weight[hits->first[ent] + __popc(members & ((1u << t) - 1))];
+            const float y0 = w * acc[0][n][t2], y1 = w * acc[0][n][2 + t2];
+            if (kNT == 1 || n == 1 || tile0 == 0) {
+              tot[n][t2] += y0;
+              tot[n][2 + t2] += y1;
+            } else {
+              tot[kNT - 1][t2] += y0;
+              tot[kNT - 1][2 + t2] += y1;
+            }
+          }
+          acc[0][n][t2] = acc[0][n][2 + t2] = 0.f;
         }
       }
     }
-    if (wk > 1) {
-      named_bar_sync(1 + group, wk * 32);
-      for (int o = part * 32 + lane; o < kMvRows * C::kCols; o += wk * 32) {
-        const int r = o % kMvRows, t = o / kMvRows;
-        const float* p = red + group * wk * C::kRed + red_at(t, r);
-        float s0 = 0.f, s1 = 0.f;
-        for (int w = 0; w < wk; ++w) {  // in warp order
-          s0 += p[w * C::kRed];
-          if constexpr (kDual) s1 += p[w * C::kRed + C::kCols * kMvRows];
-        }
-        emit(t, r, s0, s1);
-      }
-      named_bar_sync(1 + group, wk * 32);  // before the next unit's sums
+    if (cur.n && cur.u == u) continue;
+    const bool ended = cur.n || share(warp + 1) == (u - u0 + 1) * len;
+    if (mid) {
+      put(red + warp * C::kRed);
+      clear();
+    } else if (ended) {
+      each_sum([&](int t, int r, float s0, float s1) { emit(u, t, r, s0, s1); });
+      clear();
+    } else {
+      open = true;
     }
+    mid = false;
   }
   cp_async_wait<0>();
+  if (kKind == kMvDown && len == 0) {  // no expert was hit: zeros
+    const int n = ((int)((int64_t)(blockIdx.x + 1) * units / gridDim.x) - u0) * kMvRows * a.T;
+    for (int o = threadIdx.x; o < n; o += kMvThreads)
+      emit(u0 + o / (kMvRows * a.T), o / kMvRows % a.T, o % kMvRows, 0.f, 0.f);
+    return;
+  }
+  __syncthreads();
+  float* red1 = reinterpret_cast<float*>(smem);
+  static_assert(C::kRingTotal >= kMvWarps * C::kRed * 4, "the ring is large enough");
+  if (open) put(red1 + warp * C::kRed);
+  __syncthreads();
+  // A unit that is spread over warps: found at the first share that begins inside it; its sums are
+  // added in warp order.
+  constexpr int kOuts = kMvRows * C::kCols;
+  for (int w = 1 + threadIdx.x / kOuts; w < kMvWarps; w += kMvThreads / kOuts) {
+    const int o = threadIdx.x % kOuts, r = o % kMvRows, t = o / kMvRows;
+    const int p = share(w), i = p / len, begin = i * len;
+    if (p == begin || p >= total || share(w - 1) > begin) continue;  // no unit begins its spread here
+    float s0 = 0.f, s1 = 0.f;
+    for (int k = w - 1; k < kMvWarps && share(k) < begin + len; ++k) {
+      if (share(k) == share(k + 1)) continue;  // nothing
+      const float* src = (share(k) > begin ? red : red1) + k * C::kRed + red_at(t, r);
+      s0 += src[0];
+      if constexpr (kDual) s1 += src[C::kCols * kMvRows];
+    }
+    emit(u0 + i, t, r, s0, s1);
+  }
 }
 
 namespace {
