@@ -252,17 +252,16 @@ MOE_API int moe_forward_mxfp8(moe_handle *h, const void *x, int32_t T, const voi
  * codes q and zero points z in 0..15 (z = 8 where a matrix has none), bf16 scales s, and groups
  * of G = 32, 64 or 128 consecutive columns (the last one may be shorter). The library keeps it
  * in a layout of its own, two device buffers owned by the caller, 16-byte aligned:
- *   codes   moe_int4_code_bytes(R, K) bytes: blocks of 16 rows x 64 columns, 512 bytes each, at
- *           (r / 16) * ceil(K / 64) + c / 64; rows and columns past the edge are padding. In a
- *           block, the 16 bytes at (4 i + j) * 16 (i < 8, j < 4) hold the columns 8 j .. 8 j + 7 and
- *           32 + 8 j .. 32 + 8 j + 7 of rows i and i + 8: 32-bit word 2 h + m (h, m < 2) holds, from
- *           bit 0 up in steps of 4, with k = 32 h + 8 j + 4 m: (i, k), (i + 8, k), (i, k + 2),
- *           (i + 8, k + 2), (i, k + 1), (i + 8, k + 1), (i, k + 3), (i + 8, k + 3).
+ *   codes   moe_int4_code_bytes(R, K) bytes: blocks of 16 rows x 128 columns, 1024 bytes each, at
+ *           (r / 16) * ceil(K / 128) + c / 128, each two halves of 64 columns; rows and columns past
+ *           the edge are padding. In a half, the 16 bytes at (4 i + j) * 16 (i < 8, j < 4) hold the
+ *           columns 8 j .. 8 j + 7 and 32 + 8 j .. 32 + 8 j + 7 of rows i and i + 8: 32-bit word
+ *           2 h + m (h, m < 2) holds, from bit 0 up in steps of 4, with k = 32 h + 8 j + 4 m: (i, k),
+ *           (i + 8, k), (i, k + 2), (i + 8, k + 2), (i, k + 1), (i + 8, k + 1), (i, k + 3), (i + 8, k + 3).
  *   scales  moe_int4_scale_bytes(R, K, G, zeros) bytes, an entry per row and group: the bf16 scale or,
- *           with zero points, 32 bits: the scale (low half) and bf16(128 + z) (high half). Row r's
- *           entry of group g is at (r / 16) * 16 * N + n with, for G = 64 or 128, N = ceil(K / G) and
- *           n = 16 g + 2 (r % 8) + r % 16 / 8; for G = 32, N = 2 ceil(K / 64) and
- *           n = 32 (g / 2) + 4 (r % 8) + 2 (g % 2) + r % 16 / 8.
+ *           with zero points, 32 bits: the scale (low half) and bf16(128 + z) (high half). With
+ *           N = 128 / G, row r's entry of group g is at (r / 16) * 16 * N * ceil(K / 128) +
+ *           16 N (g / N) + 2 N (r % 8) + 2 (g % N) + r % 16 / 8.
  * moe_quantize_int4 and moe_pack_int4 write it. Products are exact in fp32 up to the order and
  * rounding of fp32 sums; the order is fixed, so equal inputs give equal bits. Meant for few
  * tokens, where the weights' bytes are the cost (prefill: moe_forward with bf16 weights). */

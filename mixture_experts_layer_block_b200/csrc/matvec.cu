@@ -6,8 +6,8 @@
 //    over all experts that were hit, whose K blocks then follow one another). A CTA (one to an SM) has
 //    a run of units, and its 16 warps split the run's K blocks evenly, whatever the units' number and
 //    length;
-//  - each lane copies its own 16-byte pieces of weights to shared memory with cp.async, a fixed number
-//    of blocks ahead and across unit boundaries, and reads only its own: no barrier in the K loop;
+//  - each warp copies its weights to a ring of its own in shared memory with cp.async, a fixed number of
+//    blocks ahead and across unit boundaries: no barrier of the CTA in the K loop;
 //  - the products run on mma.sync m16n8k16 (fp32 accumulation): weights come out of a register
 //    unpacking as the A fragment, tokens are the N columns. tcgen05 would need the unpacked weights
 //    written back to shared memory, for products that take a fraction of the copy's time anyway;
@@ -29,13 +29,12 @@ namespace {
 constexpr int kMvSmem = 227 * 1024;      // shared memory of an SM that CTAs can use
 constexpr int kMvMaxDepth = 12;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-  const uint32_t n = in ? 16u : 0u;  // 0: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int kBytes>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+__device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const void* src, bool in) {
+  const uint32_t n = in ? 16u : 0u;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -70,16 +69,20 @@ struct Hits {
 constexpr int kMvWarps = 16;  // one CTA to an SM
 constexpr int kMvThreads = kMvWarps * 32;
 
-template <bool kW4, bool kDual, int kKind, int kNT, bool kG32, bool kZeros>
+// kGroup: columns to a scale, 0 for bf16 weights.
+template <bool kDual, int kKind, int kNT, int kGroup, bool kZeros>
 struct Mv {
+  static constexpr bool kW4 = kGroup != 0;
   static constexpr int kMats = kDual ? 2 : 1;
-  static constexpr int kGroups = kG32 ? 2 : 1;                        // groups of a K block
-  static constexpr int kLane = kW4 ? 16 : 64;                         // weight bytes of a lane and block
-  static constexpr int kMeta = kW4 ? (kZeros ? 8 : 4) * kGroups : 0;  // scale bytes of a lane and block
-  static constexpr int kMat = 32 * (kLane + kMeta);                   // bytes of a warp's block of a matrix
+  static constexpr int kCols = kW4 ? kInt4Cols : 64;     // columns of a K block
+  static constexpr int kVecs = kCols / 64;               // 16-byte vectors of a lane's activations in half a block
+  static constexpr int kParts = kW4 ? kInt4Cols / kGroup : 1;        // groups of a block
+  static constexpr int kMeta = kW4 ? (kZeros ? 8 : 4) * kParts : 0;  // scale bytes of a lane and block
+  static constexpr int kCodes = kW4 ? 1024 : 2048;                   // weight bytes of a warp's block
+  static constexpr int kMat = kCodes + 8 * kMeta;                    // with its scales
   static constexpr int kStage = kMats * kMat;
-  static constexpr int kCols = kNT * 8;
-  static constexpr int kRed = kMats * kCols * kMvRows;                // floats of a warp's partial sums
+  static constexpr int kTok = kNT * 8;
+  static constexpr int kRed = kMats * kTok * kMvRows;                // floats of a warp's partial sums
   static constexpr int kRest = kMvWarps * kRed * (int)sizeof(float) + (kKind != kMvOne ? (int)sizeof(Hits) : 0);
   static constexpr int kDepth = std::min(kMvMaxDepth, (kMvSmem - 1024 - kRest) / (kMvWarps * kStage));
   static constexpr int kRingTotal = kMvWarps * kStage * kDepth;
@@ -178,7 +181,7 @@ __device__ __forceinline__ void build_hits(const MvArgs& a, Hits* hits, uint32_t
 }
 
 // What lanes without a token read in place of its activations.
-__device__ const uint4 kMvZeros[8] = {};
+__device__ const uint4 kMvZeros[16] = {};
 
 // A sum's place in a warp's partial sums: 16 rows to a token, rotated so that the four tokens that a
 // quarter warp writes at once fall into different banks.
@@ -186,9 +189,10 @@ __device__ __forceinline__ int red_at(int col, int row) { return col * kMvRows +
 
 }  // namespace
 
-template <bool kW4, bool kDual, int kKind, int kNT, bool kG32, bool kZeros>
+template <bool kDual, int kKind, int kNT, int kGroup, bool kZeros>
 __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant__ MvArgs a) {
-  using C = Mv<kW4, kDual, kKind, kNT, kG32, kZeros>;
+  using C = Mv<kDual, kKind, kNT, kGroup, kZeros>;
+  constexpr bool kW4 = C::kW4;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = lane >> 2, c = lane & 3;
@@ -205,17 +209,19 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     nhit = hits->n;
   }
 
-  const int tiles = ceil_div(a.m.R, kMvRows), nb = ceil_div(a.m.K, kMvBK);
-  const int stiles = ceil_div(a.shared.R, kMvRows), snb = ceil_div(a.shared.K, kMvBK);
+  const int tiles = ceil_div(a.m.R, kMvRows), nb = ceil_div(a.m.K, C::kCols);
+  const int stiles = ceil_div(a.shared.R, kMvRows), snb = ceil_div(a.shared.K, C::kCols);
   const int routed = kKind == kMvUp ? nhit * tiles : tiles;  // units of the routed experts
   const int units = kKind == kMvUp ? routed + stiles : tiles;
 
   // This CTA's units, its K blocks one after another (each unit has as many), and this warp's even
   // share of them: whole units, but for the first and the last.
-  const int u0 = (int)((int64_t)blockIdx.x * units / gridDim.x);
+  const int each = units / (int)gridDim.x, more = units - each * (int)gridDim.x;
+  const int u0 = blockIdx.x * each + min((int)blockIdx.x, more);
+  const int mine = each + ((int)blockIdx.x < more ? 1 : 0);
   const int len = kKind == kMvDown ? nhit * nb + snb : nb;
-  const int total = ((int)((int64_t)(blockIdx.x + 1) * units / gridDim.x) - u0) * len;
-  auto share = [&](int w) { return (int)((int64_t)w * total / kMvWarps); };  // where warp w's begins
+  const int total = mine * len;
+  auto share = [&](int w) { return (int)((uint64_t)w * (uint32_t)total / kMvWarps); };  // where warp w's begins
 
   auto set_segment = [&](Walk& p, int left) {  // p.u, p.ent and p.kb are set; `left` blocks of the share
     const int seg = (kKind != kMvOne && p.ent == nhit ? snb : nb) - p.kb;
@@ -251,7 +257,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   const uint8_t* sp[C::kMats];   // 4-bit: scales; bf16: row q + 8
   bool in0 = true, in1 = true;   // bf16: rows q and q + 8 exist
   int wcols = 0;                 // bf16: columns from this lane's first one to the end of the matrix
-  int half = 0;                  // 4-bit, groups of 128: the block's half of its group's columns
   auto aim_weights = [&]() {
     if (prod.n == 0) return;
     const bool sh = kKind != kMvOne && prod.ent == nhit;
@@ -261,20 +266,15 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
-        const int64_t at = (int64_t)e * ((m.R + kMvRows - 1) / kMvRows) + tile;
-        wp[i] = static_cast<const uint8_t*>(m.w[i]) + (at * (sh ? snb : nb) + prod.kb) * 512 + lane * 16;
-        // a copy brings a lane the entries of a whole K block (of two, with groups of 128)
-        const bool wide = !kG32 && a.group == 128;
-        const int per = wide ? (m.K + 127) >> 7 : (m.K + 63) >> 6;
-        sp[i] = static_cast<const uint8_t*>(m.scales[i]) + (at * per + (wide ? prod.kb >> 1 : prod.kb)) * (8 * C::kMeta) +
-                q * C::kMeta;
-        half = prod.kb & 1;
+        const int64_t at = ((int64_t)e * (sh ? stiles : tiles) + tile) * (sh ? snb : nb) + prod.kb;
+        wp[i] = static_cast<const uint8_t*>(m.w[i]) + at * C::kCodes + lane * 16;
+        sp[i] = static_cast<const uint8_t*>(m.scales[i]) + at * (8 * C::kMeta) + lane * 16;
       } else {
         const int row = tile * kMvRows + q;
         in0 = row < m.R;
         in1 = row + 8 < m.R;
         const uint16_t* w = static_cast<const uint16_t*>(m.w[i]);
-        const int64_t col = prod.kb * kMvBK + 8 * c;
+        const int64_t col = prod.kb * C::kCols + 8 * c;
         wp[i] = reinterpret_cast<const uint8_t*>(w + (in0 ? (int64_t)row * m.K : 0) + col);
         sp[i] = reinterpret_cast<const uint8_t*>(w + (in1 ? (int64_t)(row + 8) * m.K : 0) + col);
         wcols = m.K - (int)col;
@@ -286,23 +286,24 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
-        cp_async16(dst + i * C::kMat, wp[i], true);
-        wp[i] += 512;
-        cp_async_small<C::kMeta>(dst + i * C::kMat + 512 - lane * (16 - C::kMeta), sp[i]);
-        if (kG32 || a.group != 128 || half) sp[i] += 8 * C::kMeta;
+        cp_async16(dst + i * C::kMat, wp[i]);
+        cp_async16(dst + i * C::kMat + 512, wp[i] + 512);
+        if (lane < C::kMeta / 2) cp_async16(dst + i * C::kMat + 1024, sp[i]);  // 8 * kMeta bytes
+        wp[i] += C::kCodes;
+        sp[i] += 8 * C::kMeta;
       } else {
         // a piece outside the matrix is zeros; K is a multiple of 8, so that pieces are whole
         const bool k0 = wcols > 0, k1 = wcols > 32;
-        cp_async16(dst + (i * 4 + 0) * 512, k0 ? wp[i] : static_cast<const uint8_t*>(a.m.w[i]), in0 && k0);
-        cp_async16(dst + (i * 4 + 1) * 512, k1 ? wp[i] + 64 : static_cast<const uint8_t*>(a.m.w[i]), in0 && k1);
-        cp_async16(dst + (i * 4 + 2) * 512, k0 ? sp[i] : static_cast<const uint8_t*>(a.m.w[i]), in1 && k0);
-        cp_async16(dst + (i * 4 + 3) * 512, k1 ? sp[i] + 64 : static_cast<const uint8_t*>(a.m.w[i]), in1 && k1);
-        wp[i] += 128;
-        sp[i] += 128;
+        const void* any = a.m.w[i];
+        cp_async16_or_zeros(dst + (i * 4 + 0) * 512, k0 ? wp[i] : any, in0 && k0);
+        cp_async16_or_zeros(dst + (i * 4 + 1) * 512, k1 ? wp[i] + 64 : any, in0 && k1);
+        cp_async16_or_zeros(dst + (i * 4 + 2) * 512, k0 ? sp[i] : any, in1 && k0);
+        cp_async16_or_zeros(dst + (i * 4 + 3) * 512, k1 ? sp[i] + 64 : any, in1 && k1);
+        wp[i] += 2 * C::kCols;
+        sp[i] += 2 * C::kCols;
       }
     }
-    if constexpr (kW4) half ^= 1;
-    else wcols -= kMvBK;
+    if constexpr (!kW4) wcols -= C::kCols;
     if (--prod.n == 0) {
       next_segment(prod);
       aim_weights();
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     const bool sh = kKind != kMvOne && nxt.ent == nhit;
     const uint32_t members = tokens_of(nxt.ent);
     const int tile0 = kNT == 2 && (members & 0xffu) == 0 ? 1 : 0;
-    const int col = nxt.kb * kMvBK + 8 * c;
+    const int col = nxt.kb * C::kCols + 8 * c;
     xk = (sh ? a.shared.K : a.m.K) - col;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
@@ -336,29 +337,35 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
         row = sh ? a.T * a.k + t : hits->first[nxt.ent] + __popc(members & ((1u << t) - 1));
       const bool in = t < 8 * kNT && (members >> t & 1);
       xp[n] = in ? a.x + row * a.ldx + col : reinterpret_cast<const uint16_t*>(kMvZeros);
-      xstep[n] = in ? kMvBK : 0;
+      xstep[n] = in ? C::kCols : 0;
     }
     if constexpr (kNT == 2 && kKind != kMvOne) xtiles = (members & 0xffu) != 0 && members > 0xffu ? 2 : 1;
   };
-  auto load_x = [&](uint4 (&x)[kNT][2]) {  // the next block's, if there is one
+  auto load_x = [&](uint4 (&x)[kNT][C::kVecs], int h) {  // half h of the block that nxt is at
     if (nxt.n == 0) return;
     // plain loads: the warps of an SM share the rows through L1
-    if (xk + 8 * c >= kMvBK) {  // the block is whole (the same for every lane)
+    if (xk + 8 * c >= C::kCols) {  // the block is whole (the same for every lane)
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         if (n >= xtiles) break;
-        x[n][0] = *reinterpret_cast<const uint4*>(xp[n]);
-        x[n][1] = *reinterpret_cast<const uint4*>(xp[n] + 32);
-        xp[n] += xstep[n];
+#pragma unroll
+        for (int v = 0; v < C::kVecs; ++v)
+          x[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs * h + v));
       }
     } else {
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        x[n][0] = xk > 0 ? *reinterpret_cast<const uint4*>(xp[n]) : make_uint4(0, 0, 0, 0);
-        x[n][1] = xk > 32 ? *reinterpret_cast<const uint4*>(xp[n] + 32) : make_uint4(0, 0, 0, 0);
-      }
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int v = 0; v < C::kVecs; ++v)
+          x[n][v] = xk > 32 * (C::kVecs * h + v) ? *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs * h + v))
+                                                 : make_uint4(0, 0, 0, 0);
     }
-    xk -= kMvBK;
+  };
+  auto advance_x = [&]() {
+    if (nxt.n == 0) return;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) xp[n] += xstep[n];
+    xk -= C::kCols;
     if (--nxt.n == 0) {
       next_segment(nxt);
       aim_x();
@@ -383,96 +390,102 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   uint32_t members = 0;
   int tile0 = 0;
   bool both = kNT == 2;
-  // One block: the copy of a later one, the next one's activations, and its products.
-  auto block = [&](const uint4 (&x)[kNT][2], uint4 (&xnext)[kNT][2]) {
-    if (prod.n) copy(slot_in);
-    cp_async_commit();
-    slot_in += C::kStage;
-    if (slot_in == C::kStage * C::kDepth) slot_in = 0;
-    load_x(xnext);
-    cp_async_wait<C::kDepth - 1>();
-    const uint8_t* st = ring_p + slot;
-    slot += C::kStage;
-    if (slot == C::kStage * C::kDepth) slot = 0;
+  uint4 xa[kNT][C::kVecs], xb[kNT][C::kVecs];  // halves of a block: first, second
+  // Half h of a block's products; 4-bit: one half holds kParts / 2 groups, or half of the one.
+  float part[C::kMats][kNT][4];  // 4-bit: sums of the current group, not scaled
+  auto products = [&](const uint8_t* st, const uint4 (&x)[kNT][C::kVecs], int h) {
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
-        const uint4 w4 = *reinterpret_cast<const uint4*>(st + i * C::kMat + lane * 16);
+        const uint4 w4 = *reinterpret_cast<const uint4*>(st + i * C::kMat + h * 512 + lane * 16);
         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        const uint8_t* meta = st + i * C::kMat + 512 + lane * C::kMeta;
-        uint32_t mv[C::kMeta / 4];
-        if constexpr (C::kMeta == 16) {
+        constexpr int kHere = C::kParts >= 2 ? C::kParts / 2 : 1;  // groups of this half
+        constexpr int kWords = 4 / kHere;
+        const uint8_t* meta = st + i * C::kMat + 1024 + q * C::kMeta + (C::kParts >= 2 ? h * (C::kMeta / 2) : 0);
+        constexpr int kMetaWords = kHere * (kZeros ? 2 : 1);
+        uint32_t mv[kMetaWords];
+        if constexpr (kMetaWords == 4) {
           const uint4 v = *reinterpret_cast<const uint4*>(meta);
           mv[0] = v.x; mv[1] = v.y; mv[2] = v.z; mv[3] = v.w;
-        } else if constexpr (C::kMeta == 8) {
+        } else if constexpr (kMetaWords == 2) {
           const uint2 v = *reinterpret_cast<const uint2*>(meta);
           mv[0] = v.x; mv[1] = v.y;
         } else {
           mv[0] = *reinterpret_cast<const uint32_t*>(meta);
         }
 #pragma unroll
-        for (int g2 = 0; g2 < C::kGroups; ++g2) {
+        for (int g = 0; g < kHere; ++g) {
           float s0, s1;                            // rows q and q + 8
           uint32_t z0 = 0x43084308u, z1 = z0;      // bf16x2 of 128 + zero
           if constexpr (kZeros) {
-            s0 = __uint_as_float(mv[2 * g2] << 16);
-            s1 = __uint_as_float(mv[2 * g2 + 1] << 16);
-            z0 = __byte_perm(mv[2 * g2], 0, 0x3232);
-            z1 = __byte_perm(mv[2 * g2 + 1], 0, 0x3232);
+            s0 = __uint_as_float(mv[2 * g] << 16);
+            s1 = __uint_as_float(mv[2 * g + 1] << 16);
+            z0 = __byte_perm(mv[2 * g], 0, 0x3232);
+            z1 = __byte_perm(mv[2 * g + 1], 0, 0x3232);
           } else {
-            s0 = __uint_as_float(mv[g2] << 16);
-            s1 = __uint_as_float(mv[g2] & 0xffff0000u);
+            s0 = __uint_as_float(mv[g] << 16);
+            s1 = __uint_as_float(mv[g] & 0xffff0000u);
           }
-          constexpr int kWords = 4 / C::kGroups;
           uint32_t f[kWords][4];
 #pragma unroll
           for (int jj = 0; jj < kWords; ++jj)
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-              f[jj][n] = sub_bf16x2(((w[2 * g2 + jj] >> (4 * n)) & 0x000f000fu) | 0x43004300u, (n & 1) ? z1 : z0);
+              f[jj][n] = sub_bf16x2(((w[g * kWords + jj] >> (4 * n)) & 0x000f000fu) | 0x43004300u, (n & 1) ? z1 : z0);
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
             if (n == 1 && !both) break;
-            float part[4] = {};
+            float(&p)[4] = part[i][n];
+            if (C::kParts >= 2 || h == 0) p[0] = p[1] = p[2] = p[3] = 0.f;
 #pragma unroll
             for (int jj = 0; jj < kWords; ++jj) {
-              const int j = 2 * g2 + jj;
+              const int j = g * kWords + jj;
               const uint4 v = x[n][j >> 1];
-              if (j & 1) mma_bf16(part, f[jj], v.z, v.w);
-              else mma_bf16(part, f[jj], v.x, v.y);
+              if (j & 1) mma_bf16(p, f[jj], v.z, v.w);
+              else mma_bf16(p, f[jj], v.x, v.y);
             }
-            acc[i][n][0] += s0 * part[0];
-            acc[i][n][1] += s0 * part[1];
-            acc[i][n][2] += s1 * part[2];
-            acc[i][n][3] += s1 * part[3];
+            if (C::kParts >= 2 || h == 1) {
+              acc[i][n][0] += s0 * p[0];
+              acc[i][n][1] += s0 * p[1];
+              acc[i][n][2] += s1 * p[2];
+              acc[i][n][3] += s1 * p[3];
+            }
           }
         }
       } else {
-        uint4 w[2][2];  // rows q, q + 8; halves of the block
+        // rows q and q + 8 of this half
+        const uint4 lo = *reinterpret_cast<const uint4*>(st + (i * 4 + h) * 512 + lane * 16);
+        const uint4 hi = *reinterpret_cast<const uint4*>(st + (i * 4 + 2 + h) * 512 + lane * 16);
+        const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
 #pragma unroll
-        for (int r2 = 0; r2 < 2; ++r2)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            w[r2][h] = *reinterpret_cast<const uint4*>(st + (i * 4 + r2 * 2 + h) * 512 + lane * 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 lo = w[0][j >> 1], hi = w[1][j >> 1];
-          const uint32_t f[4] = {(j & 1) ? lo.z : lo.x, (j & 1) ? hi.z : hi.x, (j & 1) ? lo.w : lo.y,
-                                 (j & 1) ? hi.w : hi.y};
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            const uint4 v = x[n][j >> 1];
-            if (j & 1) mma_bf16(acc[i][n], f, v.z, v.w);
-            else mma_bf16(acc[i][n], f, v.x, v.y);
-          }
+        for (int n = 0; n < kNT; ++n) {
+          mma_bf16(acc[i][n], f0, x[n][0].x, x[n][0].y);
+          mma_bf16(acc[i][n], f1, x[n][0].z, x[n][0].w);
         }
       }
     }
   };
+  // One block: the copy of a later one, activations half a block ahead, and its products. The lanes
+  // share a block's scales, so that the copy into the slot of the block before waits for them all.
+  auto block = [&]() {
+    load_x(xb, 1);
+    cp_async_wait<C::kDepth - 2>();
+    __syncwarp();
+    if (prod.n) copy(slot_in);
+    cp_async_commit();
+    slot_in += C::kStage;
+    if (slot_in == C::kStage * C::kDepth) slot_in = 0;
+    const uint8_t* st = ring_p + slot;
+    slot += C::kStage;
+    if (slot == C::kStage * C::kDepth) slot = 0;
+    products(st, xa, 0);
+    advance_x();
+    load_x(xa, 0);
+    products(st, xb, 1);
+  };
 
-  uint4 xa[kNT][2], xb[kNT][2];
   aim_x();
-  load_x(xa);
+  load_x(xa, 0);
   auto emit = [&](int u, int t, int r, float s0, float s1) {  // output row r of unit u, token t
     int tile = u, R = a.m.R;
     int64_t row = t;
@@ -528,16 +541,18 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   auto put = [&](float* dst) {
     each_sum([&](int t, int r, float s0, float s1) {
       dst[red_at(t, r)] = s0;
-      if constexpr (kDual) dst[C::kCols * kMvRows + red_at(t, r)] = s1;
+      if constexpr (kDual) dst[C::kTok * kMvRows + red_at(t, r)] = s1;
     });
   };
 
   // Units that this warp computes whole go straight to memory. Of a unit that begins in another
   // warp's share the sums go to `red`; those of one that ends in another's stay in registers until
   // every warp is done with the ring, and go there.
-  bool open = false;  // the registers hold the beginning of a unit that another warp ends
-  bool mid = first % max(len, 1) != 0;
+  const bool one = mine == 1;  // a single unit: every warp's sums go to `red`, zeros too
+  bool open = false;           // the registers hold the beginning of a unit that another warp ends
+  bool mid = one || first % max(len, 1) != 0;
   clear();
+  if (one && cur.n == 0) put(red + warp * C::kRed);
 #pragma unroll 1
   while (cur.n) {
     members = tokens_of(cur.ent);
@@ -545,20 +560,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       tile0 = (members & 0xffu) == 0 ? 1 : 0;
       both = (members & 0xffu) != 0 && members > 0xffu;
     }
-    int n = cur.n;
 #pragma unroll 1
-    for (; n >= 2; n -= 2) {
-      block(xa, xb);
-      block(xb, xa);
-    }
-    if (n) {
-      block(xa, xb);
-#pragma unroll
-      for (int i = 0; i < kNT; ++i) {
-        xa[i][0] = xb[i][0];
-        xa[i][1] = xb[i][1];
-      }
-    }
+    for (int n = cur.n; n > 0; --n) block();
     const int ent = cur.ent;
     const int u = cur.u;
     next_segment(cur);
@@ -599,19 +602,33 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   }
   cp_async_wait<0>();
   if (kKind == kMvDown && len == 0) {  // no expert was hit: zeros
-    const int n = ((int)((int64_t)(blockIdx.x + 1) * units / gridDim.x) - u0) * kMvRows * a.T;
+    const int n = mine * kMvRows * a.T;
     for (int o = threadIdx.x; o < n; o += kMvThreads)
       emit(u0 + o / (kMvRows * a.T), o / kMvRows % a.T, o % kMvRows, 0.f, 0.f);
     return;
   }
   __syncthreads();
+  constexpr int kOuts = kMvRows * C::kTok;
+  if (one) {
+    const int o = threadIdx.x, r = o % kMvRows, t = o / kMvRows;
+    if (o < kOuts) {
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMvWarps; ++w) {
+        const float* src = red + w * C::kRed + red_at(t, r);
+        s0 += src[0];
+        if constexpr (kDual) s1 += src[C::kTok * kMvRows];
+      }
+      emit(u0, t, r, s0, s1);
+    }
+    return;
+  }
   float* red1 = reinterpret_cast<float*>(smem);
   static_assert(C::kRingTotal >= kMvWarps * C::kRed * 4, "the ring is large enough");
   if (open) put(red1 + warp * C::kRed);
   __syncthreads();
   // A unit that is spread over warps: found at the first share that begins inside it; its sums are
   // added in warp order.
-  constexpr int kOuts = kMvRows * C::kCols;
   for (int w = 1 + threadIdx.x / kOuts; w < kMvWarps; w += kMvThreads / kOuts) {
     const int o = threadIdx.x % kOuts, r = o % kMvRows, t = o / kMvRows;
     const int p = share(w), i = p / len, begin = i * len;
@@ -621,7 +638,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       if (share(k) == share(k + 1)) continue;  // nothing
       const float* src = (share(k) > begin ? red : red1) + k * C::kRed + red_at(t, r);
       s0 += src[0];
-      if constexpr (kDual) s1 += src[C::kCols * kMvRows];
+      if constexpr (kDual) s1 += src[C::kTok * kMvRows];
     }
     emit(u0 + i, t, r, s0, s1);
   }
@@ -629,39 +646,42 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 
 namespace {
 
-template <bool kW4, bool kDual, int kKind, int kNT, bool kG32, bool kZeros>
+template <bool kDual, int kKind, int kNT, int kGroup, bool kZeros>
 cudaError_t launch_mv(const MvArgs& a, int64_t units, int num_sms, cudaStream_t stream) {
-  using C = Mv<kW4, kDual, kKind, kNT, kG32, kZeros>;
-  auto* k = mv_kernel<kW4, kDual, kKind, kNT, kG32, kZeros>;
+  using C = Mv<kDual, kKind, kNT, kGroup, kZeros>;
+  auto* k = mv_kernel<kDual, kKind, kNT, kGroup, kZeros>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(units, num_sms));
   return launch_k(k, dim3(grid), dim3(kMvThreads), C::kSmem, stream, a);
 }
 
-template <bool kDual, int kKind, bool kG32, bool kZeros>
+template <bool kDual, int kKind, int kGroup, bool kZeros>
 cudaError_t pick_nt(const MvArgs& a, int64_t units, int num_sms, cudaStream_t stream) {
-  return a.T <= 8 ? launch_mv<true, kDual, kKind, 1, kG32, kZeros>(a, units, num_sms, stream)
-                  : launch_mv<true, kDual, kKind, 2, kG32, kZeros>(a, units, num_sms, stream);
+  return a.T <= 8 ? launch_mv<kDual, kKind, 1, kGroup, kZeros>(a, units, num_sms, stream)
+                  : launch_mv<kDual, kKind, 2, kGroup, kZeros>(a, units, num_sms, stream);
+}
+
+template <bool kDual, int kKind, bool kZeros>
+cudaError_t pick_group(const MvArgs& a, int64_t units, int num_sms, cudaStream_t stream) {
+  if (a.group == 32) return pick_nt<kDual, kKind, 32, kZeros>(a, units, num_sms, stream);
+  if (a.group == 64) return pick_nt<kDual, kKind, 64, kZeros>(a, units, num_sms, stream);
+  return pick_nt<kDual, kKind, 128, kZeros>(a, units, num_sms, stream);
 }
 
 template <bool kDual, int kKind>
 cudaError_t pick_int4(const MvArgs& a, bool zeros, int64_t units, int num_sms, cudaStream_t stream) {
-  if (a.group == 32)
-    return zeros ? pick_nt<kDual, kKind, true, true>(a, units, num_sms, stream)
-                 : pick_nt<kDual, kKind, true, false>(a, units, num_sms, stream);
-  return zeros ? pick_nt<kDual, kKind, false, true>(a, units, num_sms, stream)
-               : pick_nt<kDual, kKind, false, false>(a, units, num_sms, stream);
+  return zeros ? pick_group<kDual, kKind, true>(a, units, num_sms, stream)
+               : pick_group<kDual, kKind, false>(a, units, num_sms, stream);
 }
 
 // ---- laying out 4-bit matrices ----------------------------------------------------------------
-// One warp per 16 rows x 128 columns (two K blocks): lane 4 q + c holds its pieces of both blocks,
-// 64 values of rows q and q + 8 as v[block][half][row][column]. Writes the codes' words.
-__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t tile, int nb, int kb0, const uint8_t (&v)[2][2][2][8]) {
+// One warp per block of 16 rows x 128 columns: lane 4 q + c holds its pieces of both halves, 64 values
+// of rows q and q + 8 as v[half][h][row][column]. Writes the codes' words.
+__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t block, const uint8_t (&v)[2][2][2][8]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    if (kb0 + b >= nb) break;
     uint32_t w[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -673,13 +693,13 @@ __device__ __forceinline__ void store_codes(uint8_t* codes, int64_t tile, int nb
           x |= (uint32_t)v[b][h][n & 1][4 * i + 2 * ((n >> 1) & 1) + (n >> 2)] << (4 * n);
         w[2 * h + i] = x;
       }
-    *reinterpret_cast<uint4*>(codes + (tile * nb + kb0 + b) * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(codes + block * 1024 + b * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-__device__ __forceinline__ void store_scale(uint8_t* scales, int64_t tile, int stored, int group, int g, int row, bool zeros,
+__device__ __forceinline__ void store_scale(uint8_t* scales, int64_t tile, int blocks, int group, int g, int row, bool zeros,
                                             uint32_t s, uint32_t zero) {
-  const int64_t o = tile * stored * kMvRows + int4_scale_at(row, g, group);
+  const int64_t o = tile * blocks * (kInt4Cols / group) * kMvRows + int4_scale_at(row, g, group);
   if (zeros)
     reinterpret_cast<uint32_t*>(scales)[o] = s | (pack_bf16x2(128.f + (float)zero, 0.f) << 16);
   else
@@ -695,12 +715,11 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const uint16_t* __re
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, q = lane >> 2, c = lane & 3;
-  const int nb = (int)int4_col_blocks(K), np = (nb + 1) / 2;
-  const int stored = (int)int4_stored_groups(K, group);
-  const int64_t tiles = int4_row_tiles(R), items = tiles * np;
+  const int nb = (int)int4_blocks(K);
+  const int64_t items = int4_row_tiles(R) * nb;
   for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * 8) {
-    const int64_t tile = it / np;
-    const int kb0 = (int)(it % np) * 2;
+    const int64_t tile = it / nb;
+    const int k0 = (int)(it % nb) * kInt4Cols;
     float f[2][2][2][8];
     float lo[4][2], hi[4][2];  // per 32 columns and row
 #pragma unroll
@@ -708,7 +727,7 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const uint16_t* __re
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int64_t row = tile * kMvRows + q + 8 * r;
-        const int k = kb0 * kMvBK + 32 * p + 8 * c;
+        const int k = k0 + 32 * p + 8 * c;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (row < R && k < K) x = __ldg(reinterpret_cast<const uint4*>(src + row * K + k));
         float(&v)[8] = f[p >> 1][p & 1][r];
@@ -748,10 +767,10 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const uint16_t* __re
         for (int i = 0; i < 8; ++i)
           v[p >> 1][p & 1][r][i] =
               s > 0.f ? (uint8_t)fminf(fmaxf(rintf(__fdiv_rn(f[p >> 1][p & 1][r][i], s)) + zero, 0.f), 15.f) : (uint8_t)8;
-        const int g = (kb0 * kMvBK + 32 * p) / group;
-        if (p == first && c == 0 && g < stored) store_scale(scales, tile, stored, group, g, q + 8 * r, kZeros, sb, (uint32_t)zero);
+        const int g = (k0 + 32 * p) / group;
+        if (p == first && c == 0) store_scale(scales, tile, nb, group, g, q + 8 * r, kZeros, sb, (uint32_t)zero);
       }
-    store_codes(codes, tile, nb, kb0, v);
+    store_codes(codes, it, v);
   }
 }
 
@@ -761,36 +780,35 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const uint8_t* __restric
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, q = lane >> 2, c = lane & 3;
-  const int nb = (int)int4_col_blocks(K), np = (nb + 1) / 2, G = (int)int4_groups(K, group);
-  const int stored = (int)int4_stored_groups(K, group);
-  const int64_t tiles = int4_row_tiles(R), items = tiles * np;
+  const int nb = (int)int4_blocks(K), G = (K + group - 1) / group;
+  const int64_t items = int4_row_tiles(R) * nb;
   for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * 8) {
-    const int64_t tile = it / np;
-    const int kb0 = (int)(it % np) * 2;
+    const int64_t tile = it / nb;
+    const int k0 = (int)(it % nb) * kInt4Cols;
     uint8_t v[2][2][2][8];
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int64_t row = tile * kMvRows + q + 8 * r;
-        const int k = kb0 * kMvBK + 32 * p + 8 * c;
+        const int k = k0 + 32 * p + 8 * c;
         uint32_t x = 0;
         if (row < R && k < K) x = __ldg(reinterpret_cast<const uint32_t*>(src + row * (K / 2) + k / 2));
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[p >> 1][p & 1][r][i] = (uint8_t)(x >> (4 * i) & 15u);
-        const int g = (kb0 * kMvBK + 32 * p) / group;
-        if ((kb0 * kMvBK + 32 * p) % group == 0 && c == 0 && g < stored) {
+        const int g = (k0 + 32 * p) / group;
+        if ((k0 + 32 * p) % group == 0 && c == 0) {
           const bool in = row < R && g < G;
-          store_scale(scales, tile, stored, group, g, q + 8 * r, z != nullptr, in ? __ldg(s + row * G + g) : 0u,
+          store_scale(scales, tile, nb, group, g, q + 8 * r, z != nullptr, in ? __ldg(s + row * G + g) : 0u,
                       in && z ? __ldg(z + row * G + g) : 8u);
         }
       }
-    store_codes(codes, tile, nb, kb0, v);
+    store_codes(codes, it, v);
   }
 }
 
 int layout_grid(int64_t R, int64_t K, int num_sms) {
-  const int64_t items = int4_row_tiles(R) * ((int4_col_blocks(K) + 1) / 2);
+  const int64_t items = int4_row_tiles(R) * int4_blocks(K);
   return (int)std::max<int64_t>(1, std::min<int64_t>((items + 7) / 8, (int64_t)num_sms * 16));
 }
 
@@ -811,11 +829,8 @@ cudaError_t launch_int4_pack(const uint8_t* q, const uint16_t* s, const uint8_t*
 
 cudaError_t launch_mv_bf16(const MvArgs& a, bool dual, int num_sms, cudaStream_t stream) {
   const int64_t units = ceil_div(a.m.R, kMvRows);
-  if (dual)
-    return a.T <= 8 ? launch_mv<false, true, kMvOne, 1, false, false>(a, units, num_sms, stream)
-                    : launch_mv<false, true, kMvOne, 2, false, false>(a, units, num_sms, stream);
-  return a.T <= 8 ? launch_mv<false, false, kMvOne, 1, false, false>(a, units, num_sms, stream)
-                  : launch_mv<false, false, kMvOne, 2, false, false>(a, units, num_sms, stream);
+  return dual ? pick_nt<true, kMvOne, 0, false>(a, units, num_sms, stream)
+              : pick_nt<false, kMvOne, 0, false>(a, units, num_sms, stream);
 }
 
 cudaError_t launch_mv_int4(const MvArgs& a, int kind, bool zeros, int num_sms, cudaStream_t stream) {

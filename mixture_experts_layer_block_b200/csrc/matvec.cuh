@@ -9,38 +9,34 @@ namespace moe {
 
 constexpr int kMvTokens = 16;    // tokens of one launch
 constexpr int kMvRows = 16;      // output rows of a unit (the MMA's M)
-constexpr int kMvBK = 64;        // columns of a K block
+constexpr int kInt4Cols = 128;   // columns of a block of 4-bit codes
 constexpr int kMvMaxSlots = kMvTokens * kMaxTopK;
 
 // ---- the 4-bit format ------------------------------------------------------------------------
 // w[r][c] = scale[r][c / group] * (code[r][c] - zero[r][c / group]), code and zero 0..15 (zero 8
 // where a matrix has none), scale bf16, group 32, 64 or 128.
-// Codes are laid out for the MMA's A fragments: blocks of 16 rows x 64 columns (512 bytes), row
-// tiles outermost; in a block, lane 4 q + c of a warp owns 16 bytes: the columns 32 h + 8 c ..
-// 32 h + 8 c + 7 (h = 0, 1) of rows q and q + 8. Its 32-bit word 2 h + i holds, for the columns
-// k = 32 h + 8 c + 4 i + {0, 1, 2, 3}: bits 4 n .. 4 n + 3 for n = 0..7 are
+// Codes are laid out for the MMA's A fragments: blocks of 16 rows x 128 columns (1024 bytes), row tiles
+// outermost, each two halves of 64 columns (512 bytes). In a half, lane 4 q + c of a warp owns 16 bytes:
+// the columns 32 h + 8 c .. 32 h + 8 c + 7 (h = 0, 1) of rows q and q + 8. Its 32-bit word 2 h + i holds,
+// for the columns k = 32 h + 8 c + 4 i + {0, 1, 2, 3}: bits 4 n .. 4 n + 3 for n = 0..7 are
 //   (q, k), (q + 8, k), (q, k + 2), (q + 8, k + 2), (q, k + 1), (q + 8, k + 1), (q, k + 3), (q + 8, k + 3)
 // so that one mask of both half words gives two neighbouring columns of a row.
-// Scales: per row tile, then per K block (group 32 or 64) or pair of K blocks (128), then per q = 0..7,
-// then (group 32) per half of the block, the entries of rows q and q + 8, so that one copy brings a
-// lane all it needs. An entry is the bf16 scale, or, with zero points, the scale (low half word) and
-// bf16(128 + zero) (high half word). Groups past the last column have entries too.
+// Scales: per row tile, then per block, then per q = 0..7, then per group of the block, the entries of
+// rows q and q + 8, so that a lane's entries lie together. An entry is the bf16 scale, or, with zero
+// points, the scale (low half word) and bf16(128 + zero) (high half word). Groups past the last column
+// have entries too.
 __host__ __device__ inline int64_t int4_row_tiles(int64_t rows) { return (rows + kMvRows - 1) / kMvRows; }
-__host__ __device__ inline int64_t int4_col_blocks(int64_t cols) { return (cols + kMvBK - 1) / kMvBK; }
-__host__ __device__ inline int64_t int4_groups(int64_t cols, int group) { return (cols + group - 1) / group; }
+__host__ __device__ inline int64_t int4_blocks(int64_t cols) { return (cols + kInt4Cols - 1) / kInt4Cols; }
 __host__ __device__ inline int64_t int4_code_bytes(int64_t rows, int64_t cols) {
-  return int4_row_tiles(rows) * int4_col_blocks(cols) * 512;
-}
-// entries of a row in the library's layout: whole blocks of 64 columns (groups of 32 come in pairs)
-__host__ __device__ inline int64_t int4_stored_groups(int64_t cols, int group) {
-  return group == 32 ? 2 * int4_col_blocks(cols) : int4_groups(cols, group);
+  return int4_row_tiles(rows) * int4_blocks(cols) * (kMvRows * kInt4Cols / 2);
 }
 __host__ __device__ inline int64_t int4_scale_bytes(int64_t rows, int64_t cols, int group, bool zeros) {
-  return int4_row_tiles(rows) * int4_stored_groups(cols, group) * kMvRows * (zeros ? 4 : 2);
+  return int4_row_tiles(rows) * int4_blocks(cols) * (kInt4Cols / group) * kMvRows * (zeros ? 4 : 2);
 }
 // Entry of (row r of the tile, group g) among a tile's.
 __host__ __device__ inline int int4_scale_at(int r, int g, int group) {
-  return group == 32 ? (g >> 1) * 32 + (r & 7) * 4 + (g & 1) * 2 + (r >> 3) : g * 16 + (r & 7) * 2 + (r >> 3);
+  const int n = kInt4Cols / group;
+  return (g / n) * kMvRows * n + (r & 7) * 2 * n + (g % n) * 2 + (r >> 3);
 }
 
 // One or two matrices of equal shape (two: up and gate), bf16 [R][K] or 4-bit.

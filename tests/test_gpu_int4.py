@@ -47,8 +47,8 @@ def _pack(layer, q, s, z, group):
 def _unpack(m):
     """(codes [R, K], scales [R, G] as bf16 bits, zeros [R, G] or None) by the header's layout."""
     R, K, G = m.rows, m.cols, -(-m.cols // m.group)
-    nb = -(-K // 64)
-    w = m.codes.cpu().numpy().view(np.uint32).reshape(-1, nb, 8, 4, 2, 2)  # tile, block, i, j, h, m
+    nb = 2 * -(-K // 128)
+    w = m.codes.cpu().numpy().view(np.uint32).reshape(-1, nb, 8, 4, 2, 2)  # tile, half block, i, j, h, m
     code = np.zeros((w.shape[0], 16, nb, 64), dtype=np.uint8)
     where = [(0, 0), (8, 0), (0, 2), (8, 2), (0, 1), (8, 1), (0, 3), (8, 3)]
     for i in range(8):
@@ -58,14 +58,10 @@ def _unpack(m):
                     for n, (dr, dk) in enumerate(where):
                         code[:, i + dr, :, 32 * h + 8 * j + 4 * mm + dk] = w[:, :, i, j, h, mm] >> (4 * n) & 15
     code = code.reshape(-1, nb * 64)
-    N = 2 * nb if m.group == 32 else G
-    e = m.scales.cpu().numpy().view(np.uint32 if m.zeros else np.uint16).reshape(-1, 16 * N)
+    N = 128 // m.group
+    e = m.scales.cpu().numpy().view(np.uint32 if m.zeros else np.uint16).reshape(-1, 16 * N * (nb // 2))
     r, g = np.arange(16)[:, None], np.arange(G)[None, :]
-    if m.group == 32:
-        at = 32 * (g // 2) + 4 * (r % 8) + 2 * (g % 2) + r // 8
-    else:
-        at = 16 * g + 2 * (r % 8) + r // 8
-    rows = e[:, at].reshape(-1, G)
+    rows = e[:, 16 * N * (g // N) + 2 * N * (r % 8) + 2 * (g % N) + r // 8].reshape(-1, G)
     zero = None
     if m.zeros:
         zero = torch.from_numpy((rows >> 16).astype(np.uint16).view(np.int16)).view(torch.bfloat16).float().numpy() - 128
