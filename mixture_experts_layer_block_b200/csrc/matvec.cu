@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       }
     }
   };
-  auto copy = [&](uint32_t slot_off) {
+  auto copy_block = [&](uint32_t slot_off) {
     const uint32_t dst = ring + slot_off;
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
@@ -304,6 +304,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       }
     }
     if constexpr (!kW4) wcols -= C::kCols;
+  };
+  auto copy = [&](uint32_t slot_off) {
+    copy_block(slot_off);
     if (--prod.n == 0) {
       next_segment(prod);
       aim_weights();
@@ -319,6 +322,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   int xstep[kNT];                // elements to the next block (0: zeros)
   int xk = 0;                    // columns from this lane's first one to the end
   int xtiles = kNT;              // token tiles to load
+  int whole = 0;                 // blocks of the matrix from here on with all their columns
   auto tokens_of = [&](int ent) -> uint32_t {
     return kKind == kMvOne || ent == nhit ? (1u << a.T) - 1 : hits->mask[ent];
   };
@@ -329,6 +333,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     const int tile0 = kNT == 2 && (members & 0xffu) == 0 ? 1 : 0;
     const int col = nxt.kb * C::kCols + 8 * c;
     xk = (sh ? a.shared.K : a.m.K) - col;
+    whole = (sh ? a.shared.K : a.m.K) / C::kCols - nxt.kb;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       const int t = q + 8 * (tile0 + n);
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   auto load_x = [&](uint4 (&x)[kNT][C::kVecs], int h) {  // half h of the block that nxt is at
     if (nxt.n == 0) return;
     // plain loads: the warps of an SM share the rows through L1
-    if (xk + 8 * c >= C::kCols) {  // the block is whole (the same for every lane)
+    if (whole > 0) {
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         if (n >= xtiles) break;
@@ -366,6 +371,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 #pragma unroll
     for (int n = 0; n < kNT; ++n) xp[n] += xstep[n];
     xk -= C::kCols;
+    --whole;
     if (--nxt.n == 0) {
       next_segment(nxt);
       aim_x();
@@ -375,12 +381,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   Walk cur = prod;
   nxt = prod;
   aim_weights();
-  uint32_t slot_in = 0, slot = 0;  // byte offsets of the ring's slots
+  uint32_t slot = 0, vacant = 0;  // byte offsets in the ring: the block in use, the one used before it
 #pragma unroll 1
   for (int i = 0; i < C::kDepth - 1; ++i) {
-    if (prod.n) copy(slot_in);
+    if (prod.n) copy(vacant);
     cp_async_commit();
-    slot_in += C::kStage;
+    vacant += C::kStage;
   }
   if (a.early) griddep_wait();
   griddep_launch_dependents();
@@ -467,21 +473,55 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   };
   // One block: the copy of a later one, activations half a block ahead, and its products. The lanes
   // share a block's scales, so that the copy into the slot of the block before waits for them all.
+  auto turn = [&]() {
+    const uint32_t at = slot;
+    vacant = slot;
+    slot += C::kStage;
+    if (slot == C::kStage * C::kDepth) slot = 0;
+    return ring_p + at;
+  };
   auto block = [&]() {
     load_x(xb, 1);
     cp_async_wait<C::kDepth - 2>();
     __syncwarp();
-    if (prod.n) copy(slot_in);
+    if (prod.n) copy(vacant);
     cp_async_commit();
-    slot_in += C::kStage;
-    if (slot_in == C::kStage * C::kDepth) slot_in = 0;
-    const uint8_t* st = ring_p + slot;
-    slot += C::kStage;
-    if (slot == C::kStage * C::kDepth) slot = 0;
+    const uint8_t* st = turn();
     products(st, xa, 0);
     advance_x();
     load_x(xa, 0);
     products(st, xb, 1);
+  };
+  // The same for `t` blocks at which no segment ends (neither this one nor that of the copies) and
+  // whose following block is whole: nothing is asked in this loop.
+  auto run = [&](int t) {
+    prod.n -= t;
+    nxt.n -= t;
+    whole -= t;
+    xk -= t * C::kCols;
+#pragma unroll 1
+    for (; t > 0; --t) {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        if (n == 1 && kKind != kMvOne && xtiles == 1) break;
+#pragma unroll
+        for (int v = 0; v < C::kVecs; ++v) xb[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs + v));
+      }
+      cp_async_wait<C::kDepth - 2>();
+      __syncwarp();
+      copy_block(vacant);
+      cp_async_commit();
+      const uint8_t* st = turn();
+      products(st, xa, 0);
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        if (n == 1 && kKind != kMvOne && xtiles == 1) break;
+        xp[n] += xstep[n];
+#pragma unroll
+        for (int v = 0; v < C::kVecs; ++v) xa[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * v);
+      }
+      products(st, xb, 1);
+    }
   };
 
   aim_x();
@@ -561,7 +601,15 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       both = (members & 0xffu) != 0 && members > 0xffu;
     }
 #pragma unroll 1
-    for (int n = cur.n; n > 0; --n) block();
+    for (int n = cur.n; n > 0;) {
+      const int t = min(min(n, whole), prod.n) - 1;
+      if (t > 0) {
+        run(t);
+        n -= t;
+      }
+      block();
+      --n;
+    }
     const int ent = cur.ent;
     const int u = cur.u;
     next_segment(cur);
