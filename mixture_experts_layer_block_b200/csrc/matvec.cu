@@ -17,6 +17,7 @@
 // The sums of a unit that several warps share meet in shared memory and are added in warp order: equal
 // inputs give equal bits.
 #include <algorithm>
+#include <atomic>
 
 #include "ffn.cuh"
 #include "launch.h"
@@ -698,10 +699,24 @@ template <bool kDual, int kKind, int kNT, int kGroup, bool kZeros>
 cudaError_t launch_mv(const MvArgs& a, int64_t units, int num_sms, cudaStream_t stream) {
   using C = Mv<kDual, kKind, kNT, kGroup, kZeros>;
   auto* k = mv_kernel<kDual, kKind, kNT, kGroup, kZeros>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  // the kernel's shared-memory limit is raised at its first launch on a device; should the device have
+  // been reset since, the launch is refused once and repeated
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(units, num_sms));
-  return launch_k(k, dim3(grid), dim3(kMvThreads), C::kSmem, stream, a);
+  for (int attempt = 0;; ++attempt) {
+    if (attempt > 0 || !(raised.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      if (e != cudaSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+    e = launch_k(k, dim3(grid), dim3(kMvThreads), C::kSmem, stream, a);
+    if (e != cudaErrorInvalidValue || attempt > 0) return e;
+    cudaGetLastError();
+  }
 }
 
 template <bool kDual, int kKind, int kGroup, bool kZeros>

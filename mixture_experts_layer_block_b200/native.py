@@ -8,8 +8,9 @@ is missing this module raises on import.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
+
+import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # MOE_B200_LIBRARY may name another build of the same library (for A/B timing of builds)
@@ -70,9 +71,11 @@ class moe_int4_mat(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+_INT4_FIELDS = ("up", "gate", "down", "shared_up", "shared_gate", "shared_down")
+
+
 class moe_int4_experts(ctypes.Structure):
-    _fields_ = [(n, moe_int4_mat) for n in ("up", "gate", "down", "shared_up", "shared_gate", "shared_down")] + \
-               [("group", ctypes.c_int32), ("zeros", ctypes.c_int32)]
+    _fields_ = [(n, moe_int4_mat) for n in _INT4_FIELDS] + [("group", ctypes.c_int32), ("zeros", ctypes.c_int32)]
 
 
 # every symbol the header declares, with its C signature
@@ -173,17 +176,22 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_BF16, _F32, _U8, _I32S = (torch.bfloat16,), (torch.float32,), (torch.uint8,), (torch.int32,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
 def _is_tensor(t, name, shape, dtypes, device):
-    """Raises unless t is a contiguous CUDA tensor of this shape and one of these dtypes (names)
-    on this device: the library sees only its address."""
-    # the common case first, in as few attribute reads as it takes: a small call is as long as its checks
-    if isinstance(t, _tensor()) and t.dtype in _dtypes(dtypes) and t.shape == shape and t.is_contiguous() \
-            and t.is_cuda and t.get_device() == device:
-        return
-    if not isinstance(t, _tensor()):
+    """Raises unless t is a contiguous CUDA tensor of this shape and one of these dtypes on this
+    device: the library sees only its address."""
+    try:  # the common case in as few reads as it takes: a small call is as long as its checks
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+            return
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
-    if t.dtype not in _dtypes(dtypes):
-        raise TypeError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).split('.')[-1] for d in dtypes)}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -191,48 +199,34 @@ def _is_tensor(t, name, shape, dtypes, device):
     raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
-@functools.lru_cache(maxsize=None)
-def _tensor():
-    import torch
-    return torch.Tensor
-
-
-@functools.lru_cache(maxsize=None)
-def _dtypes(names):
-    import torch
-    return tuple(getattr(torch, n) for n in names)
-
-
-_BF16, _F32, _U8 = ("bfloat16",), ("float32",), ("uint8",)
-_BF16_F32 = ("bfloat16", "float32")
-
-
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without making a Stream object (1 us less a call), where torch has it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _raw_stream(stream, device):
     """The cudaStream_t of `stream`, or of the device's current stream."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(device) if stream is None else stream.cuda_stream
 
 
 class Int4Matrix:
     """A matrix [rows, cols] in 4 bits, in the library's layout (include/moe_b200.h): its codes and
     scales as uint8 CUDA tensors. Made by MoELayer.quantize_int4 or MoELayer.pack_int4."""
-    __slots__ = ("codes", "scales", "rows", "cols", "group", "zeros", "c")
+    __slots__ = ("codes", "scales", "rows", "cols", "group", "zeros", "device", "c")
 
     def __init__(self, rows, cols, group, zeros, device):
-        import torch
         nc, ns = lib.moe_int4_code_bytes(rows, cols), lib.moe_int4_scale_bytes(rows, cols, group, 1 if zeros else 0)
         if nc < 0 or ns < 0:
             raise ValueError("4-bit matrices have columns in a multiple of 8 and groups of 32, 64 or 128 columns: "
                              f"got {rows}x{cols} with groups of {group}")
         self.codes = torch.empty(nc, dtype=torch.uint8, device=device)
         self.scales = torch.empty(ns, dtype=torch.uint8, device=device)
-        self.rows, self.cols, self.group, self.zeros = rows, cols, group, bool(zeros)
+        self.rows, self.cols, self.group, self.zeros = rows, cols, group, 1 if zeros else 0
+        self.device = self.codes.get_device()
         self.c = moe_int4_mat(self.codes.data_ptr(), self.scales.data_ptr())
 
 
@@ -250,6 +244,7 @@ class MoELayer:
         check(lib.moe_init(ctypes.byref(self.cfg), ctypes.byref(h)), "moe_init")
         self.h = h
         self.device = self.query(13)
+        self._torch_device = torch.device("cuda", self.device)
         self.out_dtype = "bfloat16" if flags & MOE_FLAG_OUT_BF16 else "float32"
 
     def _check_out(self, out):
@@ -337,11 +332,10 @@ class MoELayer:
         return out
 
     def _int4_matrix(self, rows, cols, group, zeros, stream):
-        import torch
         if stream is None:
-            return Int4Matrix(rows, cols, group, zeros, torch.device("cuda", self.device))
+            return Int4Matrix(rows, cols, group, zeros, self._torch_device)
         with torch.cuda.stream(stream):
-            return Int4Matrix(rows, cols, group, zeros, torch.device("cuda", self.device))
+            return Int4Matrix(rows, cols, group, zeros, self._torch_device)
 
     def quantize_experts_int4(self, wts, group=128, zeros=False, stream=None):
         """The experts of a weight dict (W_up, W_gate, W_down and, with a shared expert, Ws_up, Ws_gate,
@@ -358,37 +352,36 @@ class MoELayer:
         T = x.shape[0]
         _is_tensor(x, "x", (T, w.cols), _BF16, self.device)
         _is_tensor(out, "out", (T, w.rows), _BF16_F32, self.device)
-        if w.codes.get_device() != self.device:
-            raise ValueError(f"w must be on cuda:{self.device}, got {w.codes.device}")
-        check(lib.moe_matvec_int4(self.h, x.data_ptr(), T, w.c, w.rows, w.cols, w.group, 1 if w.zeros else 0,
-                                  out.data_ptr(), 1 if out.element_size() == 2 else 0, _raw_stream(stream, self.device)),
-              "moe_matvec_int4")
+        if w.device != self.device:
+            raise ValueError(f"w must be on cuda:{self.device}, got cuda:{w.device}")
+        check(lib.moe_matvec_int4(self.h, x.data_ptr(), T, w.c, w.rows, w.cols, w.group, w.zeros, out.data_ptr(),
+                                  1 if out.element_size() == 2 else 0, _raw_stream(stream, self.device)), "moe_matvec_int4")
         return out
+
+    _EXPERT_NAMES = ("W_up", "W_gate", "W_down", "Ws_up", "Ws_gate", "Ws_down")
 
     def _int4_experts(self, wq):
         """The C struct of {name: Int4Matrix}, each checked against the layer's sizes."""
-        cfg = self.cfg
+        cfg, dev = self.cfg, self.device
         H, D, E, Ds = cfg.hidden, cfg.inter, cfg.num_experts, cfg.inter_shared
-        shapes = {"W_up": (E * D, H), "W_gate": (E * D, H), "W_down": (E * H, D)}
-        if Ds > 0:
-            shapes.update(Ws_up=(Ds, H), Ws_gate=(Ds, H), Ws_down=(H, Ds))
-        first = wq.get("W_up")
-        mats = []
-        for n in ("W_up", "W_gate", "W_down", "Ws_up", "Ws_gate", "Ws_down"):
-            if n not in shapes:
-                mats.append(moe_int4_mat())
-                continue
+        sizes = ((E * D, H), (E * D, H), (E * H, D), (Ds, H), (Ds, H), (H, Ds))
+        out = moe_int4_experts()
+        group = zeros = None
+        for n, field, (rows, cols) in zip(self._EXPERT_NAMES, _INT4_FIELDS, sizes if Ds > 0 else sizes[:3]):
             w = wq.get(n)
             if not isinstance(w, Int4Matrix):
                 raise TypeError(f"{n} must be an Int4Matrix, got {type(w).__name__}")
-            if (w.rows, w.cols) != shapes[n]:
-                raise ValueError(f"{n} must be {shapes[n][0]}x{shapes[n][1]}, got {w.rows}x{w.cols}")
-            if w.group != first.group or w.zeros != first.zeros:
+            if w.rows != rows or w.cols != cols:
+                raise ValueError(f"{n} must be {rows}x{cols}, got {w.rows}x{w.cols}")
+            if group is None:
+                group, zeros = w.group, w.zeros
+            elif w.group != group or w.zeros != zeros:
                 raise ValueError("the experts' matrices must share their group size, and have zero points or none")
-            if w.codes.get_device() != self.device:
-                raise ValueError(f"{n} must be on cuda:{self.device}, got {w.codes.device}")
-            mats.append(w.c)
-        return moe_int4_experts(*mats, first.group, 1 if first.zeros else 0)
+            if w.device != dev:
+                raise ValueError(f"{n} must be on cuda:{dev}, got cuda:{w.device}")
+            setattr(out, field, w.c)
+        out.group, out.zeros = group, zeros
+        return out
 
     def experts_int4(self, x, topk_ids, topk_w, wq, out, stream=None):
         """moe_experts_int4: the layer behind its gating. x [T, H] bf16 (T <= 16), topk_ids [T, k]
@@ -399,7 +392,7 @@ class MoELayer:
             raise ValueError("x must be [T, H] and topk_ids [T, k]")
         T, k = topk_ids.shape
         _is_tensor(x, "x", (T, self.cfg.hidden), _BF16, self.device)
-        _is_tensor(topk_ids, "topk_ids", (T, k), ("int32",), self.device)
+        _is_tensor(topk_ids, "topk_ids", (T, k), _I32S, self.device)
         _is_tensor(topk_w, "topk_w", (T, k), _F32, self.device)
         _is_tensor(out, "out", (T, self.cfg.hidden), _BF16_F32, self.device)
         check(lib.moe_experts_int4(self.h, x.data_ptr(), T, topk_ids.data_ptr(), topk_w.data_ptr(), k, w,
@@ -418,7 +411,7 @@ class MoELayer:
         _is_tensor(w_router, "w_router", (E, H), _BF16, self.device)
         if bias is not None:
             _is_tensor(bias, "bias", (E,), _F32, self.device)
-        _is_tensor(out, "out", (T, H), (self.out_dtype,), self.device)
+        _is_tensor(out, "out", (T, H), _BF16 if self.out_dtype == "bfloat16" else _F32, self.device)
         check(lib.moe_forward_int4(self.h, x.data_ptr(), T, w_router.data_ptr(), _addr(bias), w,
                                    top_k or self.cfg.top_k, out.data_ptr(), _raw_stream(stream, self.device)),
               "moe_forward_int4")
@@ -442,16 +435,15 @@ class MoELayer:
     def _ffn_workspace(self, workspace, need, stream):
         """The caller's workspace, or one for this call alone (allocated in the order of the
         call's stream, so that its memory is reused only behind the call)."""
-        import torch
         if workspace is not None:
             _is_tensor(workspace, "workspace", getattr(workspace, "shape", None), _U8, self.device)
             if workspace.numel() < need:
                 raise ValueError(f"the workspace needs {need} bytes, got {workspace.numel()}")
             return workspace
         if stream is None:
-            return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", self.device))
+            return torch.empty(need, dtype=torch.uint8, device=self._torch_device)
         with torch.cuda.stream(stream):
-            return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", self.device))
+            return torch.empty(need, dtype=torch.uint8, device=self._torch_device)
 
     @staticmethod
     def ffn_workspace_bytes(T, hidden, inter, backward=False):
