@@ -51,6 +51,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same onto zeros.
+__device__ __forceinline__ void mma_bf16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -65,6 +74,7 @@ struct Hits {
   uint16_t mask[kMvMaxSlots];
   uint16_t first[kMvMaxSlots];  // the expert's first pair
   float weight[kMvMaxSlots];    // by pair: an expert that a token names twice counts twice
+  uint8_t token[kMvMaxSlots];   // by pair
 };
 
 constexpr int kMvWarps = 16;  // one CTA to an SM
@@ -176,7 +186,11 @@ __device__ __forceinline__ void build_hits(const MvArgs& a, Hits* hits, uint32_t
         if (j < s) first = false;
         weight += w[j];
       }
-    if (first) hits->weight[hits->first[v >> 16] + __popc(mask & ((1u << t) - 1))] = weight;
+    if (first) {
+      const int pair = hits->first[v >> 16] + __popc(mask & ((1u << t) - 1));
+      hits->weight[pair] = weight;
+      hits->token[pair] = (uint8_t)t;
+    }
   }
   __syncthreads();
 }
@@ -315,9 +329,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   };
 
   // ---- activations: this lane's columns of a block for its tokens ----
-  // Tokens are the MMA's columns, in tiles of 8. Where an expert's tokens all lie in one of the two
-  // tiles, only that one is computed: `tile0` is the first tile with a token, `both` whether the
-  // other one has some too.
+  // An expert's tokens, one after another, are the MMA's columns: the second tile of 8 is computed only
+  // for an expert with more than 8.
   Walk nxt{};
   const uint16_t* xp[kNT];       // zeros where the lane has no token of this expert
   int xstep[kNT];                // elements to the next block (0: zeros)
@@ -329,23 +342,23 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   };
   auto aim_x = [&]() {
     if (nxt.n == 0) return;
-    const bool sh = kKind != kMvOne && nxt.ent == nhit;
-    const uint32_t members = tokens_of(nxt.ent);
-    const int tile0 = kNT == 2 && (members & 0xffu) == 0 ? 1 : 0;
+    const bool all = kKind == kMvOne || nxt.ent == nhit;  // every token: the one matrix, the shared expert
+    const int K = all && kKind != kMvOne ? a.shared.K : a.m.K;
+    const int count = all ? a.T : __popc(hits->mask[nxt.ent]), first = all ? 0 : hits->first[nxt.ent];
     const int col = nxt.kb * C::kCols + 8 * c;
-    xk = (sh ? a.shared.K : a.m.K) - col;
-    whole = (sh ? a.shared.K : a.m.K) / C::kCols - nxt.kb;
+    xk = K - col;
+    whole = K / C::kCols - nxt.kb;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
-      const int t = q + 8 * (tile0 + n);
-      int64_t row = t;
-      if constexpr (kKind == kMvDown)  // h's rows
-        row = sh ? a.T * a.k + t : hits->first[nxt.ent] + __popc(members & ((1u << t) - 1));
-      const bool in = t < 8 * kNT && (members >> t & 1);
+      const int i = q + 8 * n;
+      const bool in = i < count;
+      int64_t row = i;
+      if constexpr (kKind == kMvDown) row = all ? a.T * a.k + i : first + i;  // h's rows
+      else if (!all) row = in ? hits->token[first + i] : 0;
       xp[n] = in ? a.x + row * a.ldx + col : reinterpret_cast<const uint16_t*>(kMvZeros);
       xstep[n] = in ? C::kCols : 0;
     }
-    if constexpr (kNT == 2 && kKind != kMvOne) xtiles = (members & 0xffu) != 0 && members > 0xffu ? 2 : 1;
+    if constexpr (kNT == 2 && kKind != kMvOne) xtiles = count > 8 ? 2 : 1;
   };
   auto load_x = [&](uint4 (&x)[kNT][C::kVecs], int h) {  // half h of the block that nxt is at
     if (nxt.n == 0) return;
@@ -394,8 +407,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 
   float acc[C::kMats][kNT][4];   // of the current matrix
   float tot[kNT][4];             // kMvDown: router-weighted, over the experts so far
-  uint32_t members = 0;
-  int tile0 = 0;
   bool both = kNT == 2;
   uint4 xa[kNT][C::kVecs], xb[kNT][C::kVecs];  // halves of a block: first, second
   // Half h of a block's products; 4-bit: one half holds kParts / 2 groups, or half of the one.
@@ -443,12 +454,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
           for (int n = 0; n < kNT; ++n) {
             if (n == 1 && !both) break;
             float(&p)[4] = part[i][n];
-            if (C::kParts >= 2 || h == 0) p[0] = p[1] = p[2] = p[3] = 0.f;
 #pragma unroll
             for (int jj = 0; jj < kWords; ++jj) {
               const int j = g * kWords + jj;
               const uint4 v = x[n][j >> 1];
-              if (j & 1) mma_bf16(p, f[jj], v.z, v.w);
+              if (jj == 0 && (C::kParts >= 2 || h == 0)) mma_bf16_zero(p, f[jj], v.x, v.y);
+              else if (j & 1) mma_bf16(p, f[jj], v.z, v.w);
               else mma_bf16(p, f[jj], v.x, v.y);
             }
             if (C::kParts >= 2 || h == 1) {
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 
   aim_x();
   load_x(xa, 0);
-  auto emit = [&](int u, int t, int r, float s0, float s1) {  // output row r of unit u, token t
+  auto emit = [&](int u, int t, int r, float s0, float s1) {  // output row r of unit u, token (kMvUp: column) t
     int tile = u, R = a.m.R;
     int64_t row = t;
     bool in = t < a.T;
@@ -538,10 +549,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
         row = a.T * a.k + t;
       } else {
         const int ent = u / tiles;
-        const uint32_t m = hits->mask[ent];
         tile = u - ent * tiles;
-        in = m >> t & 1;
-        row = hits->first[ent] + __popc(m & ((1u << t) - 1));
+        in = t < __popc((uint32_t)hits->mask[ent]);
+        row = hits->first[ent] + t;
       }
     }
     const int col = tile * kMvRows + r;
@@ -572,11 +582,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   auto each_sum = [&](auto&& f) {
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
-      // an expert with tokens in the second tile only has its sums in the first place
-      const int at = kKind == kMvUp && kNT == 2 ? (n + tile0) & 1 : n;
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        f(8 * at + 2 * c + (v & 1), q + 8 * (v >> 1), kKind == kMvDown ? tot[n][v] : acc[0][n][v], acc[C::kMats - 1][n][v]);
+        f(8 * n + 2 * c + (v & 1), q + 8 * (v >> 1), kKind == kMvDown ? tot[n][v] : acc[0][n][v], acc[C::kMats - 1][n][v]);
     }
   };
   auto put = [&](float* dst) {
@@ -596,11 +604,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   if (one && cur.n == 0) put(red + warp * C::kRed);
 #pragma unroll 1
   while (cur.n) {
-    members = tokens_of(cur.ent);
-    if constexpr (kNT == 2 && kKind != kMvOne) {
-      tile0 = (members & 0xffu) == 0 ? 1 : 0;
-      both = (members & 0xffu) != 0 && members > 0xffu;
-    }
+    const uint32_t members = tokens_of(cur.ent);
+    if constexpr (kNT == 2 && kKind != kMvOne) both = __popc(members) > 8;
 #pragma unroll 1
     for (int n = cur.n; n > 0;) {
       const int t = min(min(n, whole), prod.n) - 1;
@@ -615,26 +620,35 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     const int u = cur.u;
     next_segment(cur);
     if constexpr (kKind == kMvDown) {
-      // the router weights of the matrix that ends here
+      // the router weights of the matrix that ends here; its columns go back to their tokens' places
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
+      for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
-          const int t = 8 * (tile0 + n) + 2 * c + t2;
-          if (t < 8 * kNT && (members >> t & 1)) {
-            const float w = ent == nhit ? 1.f : hits->weight[hits->first[ent] + __popc(members & ((1u << t) - 1))];
-            const float y0 = w * acc[0][n][t2], y1 = w * acc[0][n][2 + t2];
-            if (kNT == 1 || n == 1 || tile0 == 0) {
-              tot[n][t2] += y0;
-              tot[n][2 + t2] += y1;
-            } else {
-              tot[kNT - 1][t2] += y0;
-              tot[kNT - 1][2 + t2] += y1;
+          const int t = 8 * n + 2 * c + t2, i = __popc(members & ((1u << t) - 1));
+          const int from = (lane & ~3) | ((i & 7) >> 1);
+          float y[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float v0 = __shfl_sync(0xffffffffu, acc[0][0][2 * r], from);
+            const float v1 = __shfl_sync(0xffffffffu, acc[0][0][2 * r + 1], from);
+            y[r] = i & 1 ? v1 : v0;
+            if (kNT == 2 && both) {
+              const float w0 = __shfl_sync(0xffffffffu, acc[0][kNT - 1][2 * r], from);
+              const float w1 = __shfl_sync(0xffffffffu, acc[0][kNT - 1][2 * r + 1], from);
+              if (i >= 8) y[r] = i & 1 ? w1 : w0;
             }
           }
-          acc[0][n][t2] = acc[0][n][2 + t2] = 0.f;
+          if (t < a.T && (members >> t & 1)) {
+            const float w = ent == nhit ? 1.f : hits->weight[hits->first[ent] + i];
+            tot[n][t2] += w * y[0];
+            tot[n][2 + t2] += w * y[1];
+          }
         }
-      }
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[0][n][v] = 0.f;
     }
     if (cur.n && cur.u == u) continue;
     const bool ended = cur.n || share(warp + 1) == (u - u0 + 1) * len;
