@@ -67,12 +67,13 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // The experts of a batch: which were hit, in rising order, by which tokens, and for every (expert,
-// token) pair, in that order, the token's router weight for that expert.
+// token) pair, in that order, the token's router weight for that expert. An entry has at most 8 tokens
+// (the MMA's columns): an expert with more has two, and its weights are read twice, in turn.
 struct Hits {
   int32_t n;
   uint16_t expert[kMvMaxSlots];
   uint16_t mask[kMvMaxSlots];
-  uint16_t first[kMvMaxSlots];  // the expert's first pair
+  uint16_t first[kMvMaxSlots];  // the entry's first pair
   float weight[kMvMaxSlots];    // by pair: an expert that a token names twice counts twice
   uint8_t token[kMvMaxSlots];   // by pair
 };
@@ -92,7 +93,8 @@ struct Mv {
   static constexpr int kCodes = kW4 ? 1024 : 2048;                   // weight bytes of a warp's block
   static constexpr int kMat = kCodes + 8 * kMeta;                    // with its scales
   static constexpr int kStage = kMats * kMat;
-  static constexpr int kTok = kNT * 8;
+  static constexpr int kXT = kKind == kMvOne ? kNT : 1;              // token tiles of a product
+  static constexpr int kTok = kKind == kMvUp ? 8 : kNT * 8;          // columns of a unit's sums
   static constexpr int kRed = kMats * kTok * kMvRows;                // floats of a warp's partial sums
   static constexpr int kRest = kMvWarps * kRed * (int)sizeof(float) + (kKind != kMvOne ? (int)sizeof(Hits) : 0);
   static constexpr int kDepth = std::min(kMvMaxDepth, (kMvSmem - 1024 - kRest) / (kMvWarps * kStage));
@@ -116,8 +118,8 @@ constexpr int hit_scratch(int slots) { return (kMaxExperts + 32 + 2 * slots) * 4
 
 // Every thread of the CTA: the hit list of the batch. Integers only, and weights added in slot order.
 __device__ __forceinline__ void build_hits(const MvArgs& a, Hits* hits, uint32_t* scratch) {
-  uint32_t* emask = scratch;  // tokens by expert; later | index in the hit list << 16
-  int* chunk = reinterpret_cast<int*>(scratch + kMaxExperts);  // experts hit | pairs << 16, of 32 experts
+  uint32_t* emask = scratch;  // tokens by expert; later | index of the expert's first entry << 16
+  int* chunk = reinterpret_cast<int*>(scratch + kMaxExperts);  // entries | pairs << 16, of 32 experts
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.T * a.k, s = threadIdx.x;
   int* ids = chunk + 32;
@@ -137,24 +139,25 @@ __device__ __forceinline__ void build_hits(const MvArgs& a, Hits* hits, uint32_t
   __syncthreads();
   // chunks of 32 experts: warp w's are w and w + 16
   const int chunks = (a.E + 31) >> 5;
-  uint32_t m[2], any[2];
-  int sum[2];
+  uint32_t m[2];
+  int sum[2], own[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int x = (warp + kMvWarps * i) * 32 + lane;
     m[i] = x < a.E ? emask[x] : 0;
     if (a.capacity > 0)
       while (__popc(m[i]) > a.capacity) m[i] &= ~(0x80000000u >> __clz(m[i]));  // the highest token is dropped
-    any[i] = __ballot_sync(0xffffffffu, m[i] != 0);
-    sum[i] = __popc(m[i]);  // inclusive scan of the pairs
-    if (any[i]) {
+    const int n = __popc(m[i]);
+    own[i] = (n + 7) / 8 | n << 16;
+    sum[i] = own[i];  // inclusive scan
+    if (__ballot_sync(0xffffffffu, n > 0)) {
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
         const int v = __shfl_up_sync(0xffffffffu, sum[i], o);
         if (lane >= o) sum[i] += v;
       }
     }
-    if (lane == 31) chunk[warp + kMvWarps * i] = __popc(any[i]) | sum[i] << 16;
+    if (lane == 31) chunk[warp + kMvWarps * i] = sum[i];
   }
   __syncthreads();
   int before = lane < chunks ? chunk[lane] : 0;  // both counts at once: neither reaches 2^15
@@ -168,13 +171,19 @@ __device__ __forceinline__ void build_hits(const MvArgs& a, Hits* hits, uint32_t
   for (int i = 0; i < 2; ++i) {
     const int ch = warp + kMvWarps * i, x = ch * 32 + lane;
     const int base = __shfl_sync(0xffffffffu, before, ch == 0 ? 0 : ch - 1);
+    const int at = (ch ? base : 0) + sum[i] - own[i];  // entries and pairs before this expert's
     if (m[i]) {
-      const int at = (ch ? base & 0xffff : 0) + __popc(any[i] & ((1u << lane) - 1));
-      hits->expert[at] = (uint16_t)x;
-      hits->mask[at] = (uint16_t)m[i];
-      hits->first[at] = (uint16_t)((ch ? base >> 16 : 0) + sum[i] - __popc(m[i]));
+      uint32_t rest = m[i];
+      for (int n = 0; n < (own[i] & 0xffff); ++n) {
+        uint32_t part = rest;  // its lowest 8 tokens
+        while (__popc(part) > 8) part &= ~(0x80000000u >> __clz(part));
+        rest &= ~part;
+        hits->expert[(at & 0xffff) + n] = (uint16_t)x;
+        hits->mask[(at & 0xffff) + n] = (uint16_t)part;
+        hits->first[(at & 0xffff) + n] = (uint16_t)((at >> 16) + 8 * n);
+      }
     }
-    if (x < a.E) emask[x] = m[i] ? m[i] | (uint32_t)((ch ? base & 0xffff : 0) + __popc(any[i] & ((1u << lane) - 1))) << 16 : 0;
+    if (x < a.E) emask[x] = m[i] ? m[i] | (uint32_t)(at & 0xffff) << 16 : 0;
   }
   __syncthreads();
   if (in) {
@@ -226,20 +235,22 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 
   const int tiles = ceil_div(a.m.R, kMvRows), nb = ceil_div(a.m.K, C::kCols);
   const int stiles = ceil_div(a.shared.R, kMvRows), snb = ceil_div(a.shared.K, C::kCols);
-  const int routed = kKind == kMvUp ? nhit * tiles : tiles;  // units of the routed experts
-  const int units = kKind == kMvUp ? routed + stiles : tiles;
+  const int shared = kKind != kMvOne && a.shared.R > 0 ? (a.T + 7) / 8 : 0;  // entries of the shared expert: nhit ...
+  const int routed = kKind == kMvUp ? nhit * tiles : tiles;                  // units of the routed experts
+  const int units = kKind == kMvUp ? routed + shared * stiles : tiles;
 
   // This CTA's units, its K blocks one after another (each unit has as many), and this warp's even
   // share of them: whole units, but for the first and the last.
   const int each = units / (int)gridDim.x, more = units - each * (int)gridDim.x;
   const int u0 = blockIdx.x * each + min((int)blockIdx.x, more);
   const int mine = each + ((int)blockIdx.x < more ? 1 : 0);
-  const int len = kKind == kMvDown ? nhit * nb + snb : nb;
+  const int len = kKind == kMvDown ? nhit * nb + shared * snb : nb;
   const int total = mine * len;
   auto share = [&](int w) { return (int)((uint64_t)w * (uint32_t)total / kMvWarps); };  // where warp w's begins
 
+  auto entry_of = [&](int u) { return u >= routed ? nhit + (u - routed) / stiles : u / tiles; };  // kMvUp
   auto set_segment = [&](Walk& p, int left) {  // p.u, p.ent and p.kb are set; `left` blocks of the share
-    const int seg = (kKind != kMvOne && p.ent == nhit ? snb : nb) - p.kb;
+    const int seg = (kKind != kMvOne && p.ent >= nhit ? snb : nb) - p.kb;
     p.n = min(left, seg);
     p.rest = left - p.n;
   };
@@ -249,11 +260,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       return;
     }
     p.kb = 0;
-    if (kKind == kMvDown && p.ent + 1 < nhit + (snb ? 1 : 0)) {
+    if (kKind == kMvDown && p.ent + 1 < nhit + shared) {
       ++p.ent;
     } else {
       ++p.u;
-      p.ent = kKind == kMvUp ? (p.u >= routed ? nhit : p.u / tiles) : 0;
+      p.ent = kKind == kMvUp ? entry_of(p.u) : 0;
     }
     set_segment(p, p.rest);
   };
@@ -264,8 +275,13 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   if (first < share(warp + 1)) {
     const int b = first % len;
     prod.u = u0 + first / len;
-    prod.ent = kKind == kMvDown ? min(b / nb, nhit) : (kKind == kMvUp ? (prod.u >= routed ? nhit : prod.u / tiles) : 0);
-    prod.kb = kKind == kMvDown ? b - prod.ent * nb : b;
+    prod.ent = kKind == kMvUp ? entry_of(prod.u) : 0;
+    prod.kb = b;
+    if constexpr (kKind == kMvDown) {
+      const bool sh = b >= nhit * nb;
+      prod.ent = sh ? nhit + (b - nhit * nb) / snb : b / nb;
+      prod.kb = sh ? (b - nhit * nb) % snb : b % nb;
+    }
     set_segment(prod, share(warp + 1) - first);
   }
   const uint8_t* wp[C::kMats];   // 4-bit: codes; bf16: row q
@@ -274,10 +290,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   int wcols = 0;                 // bf16: columns from this lane's first one to the end of the matrix
   auto aim_weights = [&]() {
     if (prod.n == 0) return;
-    const bool sh = kKind != kMvOne && prod.ent == nhit;
+    const bool sh = kKind != kMvOne && prod.ent >= nhit;
     const MvMatrix& m = sh ? a.shared : a.m;
     const int e = kKind == kMvOne || sh ? 0 : hits->expert[prod.ent];
-    const int tile = kKind == kMvUp ? (sh ? prod.u - routed : prod.u - prod.ent * tiles) : prod.u;
+    const int tile = kKind == kMvUp ? (sh ? (prod.u - routed) % stiles : prod.u - prod.ent * tiles) : prod.u;
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
@@ -329,51 +345,51 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   };
 
   // ---- activations: this lane's columns of a block for its tokens ----
-  // An expert's tokens, one after another, are the MMA's columns: the second tile of 8 is computed only
-  // for an expert with more than 8.
+  // An entry's tokens, one after another, are the MMA's columns.
   Walk nxt{};
-  const uint16_t* xp[kNT];       // zeros where the lane has no token of this expert
-  int xstep[kNT];                // elements to the next block (0: zeros)
+  const uint16_t* xp[C::kXT];    // zeros where the lane has no token of this expert
+  int xstep[C::kXT];              // elements to the next block (0: zeros)
   int xk = 0;                    // columns from this lane's first one to the end
-  int xtiles = kNT;              // token tiles to load
   int whole = 0;                 // blocks of the matrix from here on with all their columns
   auto tokens_of = [&](int ent) -> uint32_t {
-    return kKind == kMvOne || ent == nhit ? (1u << a.T) - 1 : hits->mask[ent];
+    const uint32_t all = (1u << a.T) - 1;
+    if (kKind == kMvOne) return all;
+    return ent >= nhit ? all & 0xffu << 8 * (ent - nhit) : hits->mask[ent];
   };
   auto aim_x = [&]() {
     if (nxt.n == 0) return;
-    const bool all = kKind == kMvOne || nxt.ent == nhit;  // every token: the one matrix, the shared expert
-    const int K = all && kKind != kMvOne ? a.shared.K : a.m.K;
-    const int count = all ? a.T : __popc(hits->mask[nxt.ent]), first = all ? 0 : hits->first[nxt.ent];
+    const bool sh = kKind != kMvOne && nxt.ent >= nhit;
+    const int K = sh ? a.shared.K : a.m.K;
+    const int count = __popc(tokens_of(nxt.ent));
+    // the entry's first token (the one matrix, the shared expert) or pair
+    const int first = kKind == kMvOne ? 0 : (sh ? 8 * (nxt.ent - nhit) : hits->first[nxt.ent]);
     const int col = nxt.kb * C::kCols + 8 * c;
     xk = K - col;
     whole = K / C::kCols - nxt.kb;
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
+    for (int n = 0; n < C::kXT; ++n) {
       const int i = q + 8 * n;
       const bool in = i < count;
-      int64_t row = i;
-      if constexpr (kKind == kMvDown) row = all ? a.T * a.k + i : first + i;  // h's rows
-      else if (!all) row = in ? hits->token[first + i] : 0;
+      int64_t row = first + i;
+      if constexpr (kKind == kMvDown) row += sh ? a.T * a.k : 0;  // h's rows
+      else if (kKind == kMvUp && !sh) row = in ? hits->token[first + i] : 0;
       xp[n] = in ? a.x + row * a.ldx + col : reinterpret_cast<const uint16_t*>(kMvZeros);
       xstep[n] = in ? C::kCols : 0;
     }
-    if constexpr (kNT == 2 && kKind != kMvOne) xtiles = count > 8 ? 2 : 1;
   };
-  auto load_x = [&](uint4 (&x)[kNT][C::kVecs], int h) {  // half h of the block that nxt is at
+  auto load_x = [&](uint4 (&x)[C::kXT][C::kVecs], int h) {  // half h of the block that nxt is at
     if (nxt.n == 0) return;
     // plain loads: the warps of an SM share the rows through L1
     if (whole > 0) {
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        if (n >= xtiles) break;
+      for (int n = 0; n < C::kXT; ++n) {
 #pragma unroll
         for (int v = 0; v < C::kVecs; ++v)
           x[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs * h + v));
       }
     } else {
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int n = 0; n < C::kXT; ++n)
 #pragma unroll
         for (int v = 0; v < C::kVecs; ++v)
           x[n][v] = xk > 32 * (C::kVecs * h + v) ? *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs * h + v))
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   auto advance_x = [&]() {
     if (nxt.n == 0) return;
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) xp[n] += xstep[n];
+    for (int n = 0; n < C::kXT; ++n) xp[n] += xstep[n];
     xk -= C::kCols;
     --whole;
     if (--nxt.n == 0) {
@@ -405,13 +421,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   if (a.early) griddep_wait();
   griddep_launch_dependents();
 
-  float acc[C::kMats][kNT][4];   // of the current matrix
+  float acc[C::kMats][C::kXT][4];   // of the current matrix
   float tot[kNT][4];             // kMvDown: router-weighted, over the experts so far
-  bool both = kNT == 2;
-  uint4 xa[kNT][C::kVecs], xb[kNT][C::kVecs];  // halves of a block: first, second
+  uint4 xa[C::kXT][C::kVecs], xb[C::kXT][C::kVecs];  // halves of a block: first, second
   // Half h of a block's products; 4-bit: one half holds kParts / 2 groups, or half of the one.
-  float part[C::kMats][kNT][4];  // 4-bit: sums of the current group, not scaled
-  auto products = [&](const uint8_t* st, const uint4 (&x)[kNT][C::kVecs], int h) {
+  float part[C::kMats][C::kXT][4];  // 4-bit: sums of the current group, not scaled
+  auto products = [&](const uint8_t* st, const uint4 (&x)[C::kXT][C::kVecs], int h) {
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
@@ -451,8 +466,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
             for (int n = 0; n < 4; ++n)
               f[jj][n] = sub_bf16x2(((w[g * kWords + jj] >> (4 * n)) & 0x000f000fu) | 0x43004300u, (n & 1) ? z1 : z0);
 #pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            if (n == 1 && !both) break;
+          for (int n = 0; n < C::kXT; ++n) {
             float(&p)[4] = part[i][n];
 #pragma unroll
             for (int jj = 0; jj < kWords; ++jj) {
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
         const uint4 hi = *reinterpret_cast<const uint4*>(st + (i * 4 + 2 + h) * 512 + lane * 16);
         const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
+        for (int n = 0; n < C::kXT; ++n) {
           mma_bf16(acc[i][n], f0, x[n][0].x, x[n][0].y);
           mma_bf16(acc[i][n], f1, x[n][0].z, x[n][0].w);
         }
@@ -514,8 +528,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 #pragma unroll 1
     for (; t > 0; --t) {
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        if (n == 1 && kKind != kMvOne && xtiles == 1) break;
+      for (int n = 0; n < C::kXT; ++n) {
 #pragma unroll
         for (int v = 0; v < C::kVecs; ++v) xb[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs + v));
       }
@@ -526,8 +539,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       const uint8_t* st = turn();
       products(st, xa, 0);
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        if (n == 1 && kKind != kMvOne && xtiles == 1) break;
+      for (int n = 0; n < C::kXT; ++n) {
         xp[n] += xstep[n];
 #pragma unroll
         for (int v = 0; v < C::kVecs; ++v) xa[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * v);
@@ -544,9 +556,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     bool in = t < a.T;
     if constexpr (kKind == kMvUp) {
       if (u >= routed) {
-        tile = u - routed;
+        const int i = (u - routed) / stiles;
+        tile = (u - routed) - i * stiles;
         R = a.shared.R;
-        row = a.T * a.k + t;
+        row = a.T * a.k + 8 * i + t;
+        in = 8 * i + t < a.T;
       } else {
         const int ent = u / tiles;
         tile = u - ent * tiles;
@@ -570,22 +584,24 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   };
   auto clear = [&]() {
 #pragma unroll
-    for (int n = 0; n < kNT; ++n)
+    for (int v = 0; v < 4; ++v) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
+      for (int n = 0; n < C::kXT; ++n)
 #pragma unroll
         for (int i = 0; i < C::kMats; ++i) acc[i][n][v] = 0.f;
-        tot[n][v] = 0.f;
-      }
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) tot[n][v] = 0.f;
+    }
   };
-  // Calls f(token, row, sum, second matrix's sum) for this lane's sums of the unit.
+  // Calls f(token or column, row, sum, second matrix's sum) for this lane's sums of the unit.
   auto each_sum = [&](auto&& f) {
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
+    for (int n = 0; n < C::kTok / 8; ++n)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        f(8 * n + 2 * c + (v & 1), q + 8 * (v >> 1), kKind == kMvDown ? tot[n][v] : acc[0][n][v], acc[C::kMats - 1][n][v]);
-    }
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (kKind == kMvDown) f(8 * n + 2 * c + (v & 1), q + 8 * (v >> 1), tot[n][v], 0.f);
+        else f(8 * n + 2 * c + (v & 1), q + 8 * (v >> 1), acc[0][n][v], acc[C::kMats - 1][n][v]);
+      }
   };
   auto put = [&](float* dst) {
     each_sum([&](int t, int r, float s0, float s1) {
@@ -605,7 +621,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 #pragma unroll 1
   while (cur.n) {
     const uint32_t members = tokens_of(cur.ent);
-    if constexpr (kNT == 2 && kKind != kMvOne) both = __popc(members) > 8;
 #pragma unroll 1
     for (int n = cur.n; n > 0;) {
       const int t = min(min(n, whole), prod.n) - 1;
@@ -620,7 +635,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     const int u = cur.u;
     next_segment(cur);
     if constexpr (kKind == kMvDown) {
-      // the router weights of the matrix that ends here; its columns go back to their tokens' places
+      // the router weights of the matrix that ends here; its columns go to their tokens' places
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -633,22 +648,15 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
             const float v0 = __shfl_sync(0xffffffffu, acc[0][0][2 * r], from);
             const float v1 = __shfl_sync(0xffffffffu, acc[0][0][2 * r + 1], from);
             y[r] = i & 1 ? v1 : v0;
-            if (kNT == 2 && both) {
-              const float w0 = __shfl_sync(0xffffffffu, acc[0][kNT - 1][2 * r], from);
-              const float w1 = __shfl_sync(0xffffffffu, acc[0][kNT - 1][2 * r + 1], from);
-              if (i >= 8) y[r] = i & 1 ? w1 : w0;
-            }
           }
-          if (t < a.T && (members >> t & 1)) {
-            const float w = ent == nhit ? 1.f : hits->weight[hits->first[ent] + i];
+          if (members >> t & 1) {
+            const float w = ent >= nhit ? 1.f : hits->weight[hits->first[ent] + i];
             tot[n][t2] += w * y[0];
             tot[n][2 + t2] += w * y[1];
           }
         }
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[0][n][v] = 0.f;
+      for (int v = 0; v < 4; ++v) acc[0][0][v] = 0.f;
     }
     if (cur.n && cur.u == u) continue;
     const bool ended = cur.n || share(warp + 1) == (u - u0 + 1) * len;
@@ -735,8 +743,9 @@ cudaError_t launch_mv(const MvArgs& a, int64_t units, int num_sms, cudaStream_t 
 
 template <bool kDual, int kKind, int kGroup, bool kZeros>
 cudaError_t pick_nt(const MvArgs& a, int64_t units, int num_sms, cudaStream_t stream) {
-  return a.T <= 8 ? launch_mv<kDual, kKind, 1, kGroup, kZeros>(a, units, num_sms, stream)
-                  : launch_mv<kDual, kKind, 2, kGroup, kZeros>(a, units, num_sms, stream);
+  if constexpr (kKind != kMvUp)
+    if (a.T > 8) return launch_mv<kDual, kKind, 2, kGroup, kZeros>(a, units, num_sms, stream);
+  return launch_mv<kDual, kKind, 1, kGroup, kZeros>(a, units, num_sms, stream);
 }
 
 template <bool kDual, int kKind, bool kZeros>
@@ -914,8 +923,8 @@ cudaError_t launch_mv_int4(const MvArgs& a, int kind, bool zeros, int num_sms, c
   const int64_t tiles = ceil_div(a.m.R, kMvRows);
   if (kind == kMvOne) return pick_int4<false, kMvOne>(a, zeros, tiles, num_sms, stream);
   if (kind == kMvDown) return pick_int4<false, kMvDown>(a, zeros, tiles, num_sms, stream);
-  // at most one expert per slot
-  const int64_t units = tiles * std::min(a.E, a.T * a.k) + ceil_div(a.shared.R, kMvRows);
+  // at most an entry per slot
+  const int64_t units = tiles * a.T * a.k + 2 * ceil_div(a.shared.R, kMvRows);
   return pick_int4<true, kMvUp>(a, zeros, units, num_sms, stream);
 }
 
