@@ -109,7 +109,8 @@ struct Walk {
   int u;      // unit
   int rest;   // blocks of the share behind this segment
   int n;      // blocks of the segment from here on (0 past the share's end)
-  int ent;    // the matrix: entry of the hit list (its length: the shared expert)
+  int ent;    // the matrix: entry of the hit list (from its length on: of the shared expert)
+  int tile;   // the unit's 16-row tile of the matrix
   int kb;     // block of the matrix where the segment begins
 };
 
@@ -248,7 +249,16 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   const int total = mine * len;
   auto share = [&](int w) { return (int)((uint64_t)w * (uint32_t)total / kMvWarps); };  // where warp w's begins
 
-  auto entry_of = [&](int u) { return u >= routed ? nhit + (u - routed) / stiles : u / tiles; };  // kMvUp
+  auto locate = [&](int u, int& ent, int& tile) {  // a unit's matrix (kMvDown: the first) and tile
+    ent = 0;
+    tile = u;
+    if constexpr (kKind == kMvUp) {
+      const bool sh = u >= routed;
+      const int v = sh ? u - routed : u, n = v / (sh ? stiles : tiles);
+      ent = sh ? nhit + n : n;
+      tile = v - n * (sh ? stiles : tiles);
+    }
+  };
   auto set_segment = [&](Walk& p, int left) {  // p.u, p.ent and p.kb are set; `left` blocks of the share
     const int seg = (kKind != kMvOne && p.ent >= nhit ? snb : nb) - p.kb;
     p.n = min(left, seg);
@@ -264,7 +274,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       ++p.ent;
     } else {
       ++p.u;
-      p.ent = kKind == kMvUp ? entry_of(p.u) : 0;
+      ++p.tile;
+      if constexpr (kKind == kMvDown) p.ent = 0;
+      if (kKind == kMvUp && p.tile == (p.ent >= nhit ? stiles : tiles)) {
+        ++p.ent;
+        p.tile = 0;
+      }
     }
     set_segment(p, p.rest);
   };
@@ -273,14 +288,15 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   Walk prod{};
   const int first = share(warp);
   if (first < share(warp + 1)) {
-    const int b = first % len;
-    prod.u = u0 + first / len;
-    prod.ent = kKind == kMvUp ? entry_of(prod.u) : 0;
+    const int i = first / len, b = first - i * len;
+    prod.u = u0 + i;
+    locate(prod.u, prod.ent, prod.tile);
     prod.kb = b;
     if constexpr (kKind == kMvDown) {
       const bool sh = b >= nhit * nb;
-      prod.ent = sh ? nhit + (b - nhit * nb) / snb : b / nb;
-      prod.kb = sh ? (b - nhit * nb) % snb : b % nb;
+      const int v = sh ? b - nhit * nb : b, n = v / (sh ? snb : nb);
+      prod.ent = sh ? nhit + n : n;
+      prod.kb = v - n * (sh ? snb : nb);
     }
     set_segment(prod, share(warp + 1) - first);
   }
@@ -293,7 +309,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     const bool sh = kKind != kMvOne && prod.ent >= nhit;
     const MvMatrix& m = sh ? a.shared : a.m;
     const int e = kKind == kMvOne || sh ? 0 : hits->expert[prod.ent];
-    const int tile = kKind == kMvUp ? (sh ? (prod.u - routed) % stiles : prod.u - prod.ent * tiles) : prod.u;
+    const int tile = prod.tile;
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
@@ -550,27 +566,29 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
 
   aim_x();
   load_x(xa, 0);
-  auto emit = [&](int u, int t, int r, float s0, float s1) {  // output row r of unit u, token (kMvUp: column) t
-    int tile = u, R = a.m.R;
-    int64_t row = t;
-    bool in = t < a.T;
+  // Where a unit's results go: column or token t's row is row0 + t, for t < count; output rows below R.
+  struct Place {
+    int64_t row0;
+    int count, col0, R;
+  };
+  auto place = [&](int ent, int tile) {
+    Place p{0, a.T, tile * kMvRows, a.m.R};
     if constexpr (kKind == kMvUp) {
-      if (u >= routed) {
-        const int i = (u - routed) / stiles;
-        tile = (u - routed) - i * stiles;
-        R = a.shared.R;
-        row = a.T * a.k + 8 * i + t;
-        in = 8 * i + t < a.T;
+      if (ent >= nhit) {
+        p.R = a.shared.R;
+        p.row0 = a.T * a.k + 8 * (ent - nhit);
+        p.count = a.T - 8 * (ent - nhit);
       } else {
-        const int ent = u / tiles;
-        tile = u - ent * tiles;
-        in = t < __popc((uint32_t)hits->mask[ent]);
-        row = hits->first[ent] + t;
+        p.row0 = hits->first[ent];
+        p.count = __popc((uint32_t)hits->mask[ent]);
       }
     }
-    const int col = tile * kMvRows + r;
-    if (!in || col >= R) return;
-    const int64_t at = row * a.ldo + col;
+    return p;
+  };
+  auto emit = [&](const Place& p, int t, int r, float s0, float s1) {
+    const int col = p.col0 + r;
+    if (t >= p.count || col >= p.R) return;
+    const int64_t at = (p.row0 + t) * a.ldo + col;
     float v = s0;
     if constexpr (kDual) {
       v = swiglu(s0, s1);
@@ -631,8 +649,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       block();
       --n;
     }
-    const int ent = cur.ent;
-    const int u = cur.u;
+    const int ent = cur.ent, tile = cur.tile, u = cur.u;
     next_segment(cur);
     if constexpr (kKind == kMvDown) {
       // the router weights of the matrix that ends here; its columns go to their tokens' places
@@ -664,7 +681,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       put(red + warp * C::kRed);
       clear();
     } else if (ended) {
-      each_sum([&](int t, int r, float s0, float s1) { emit(u, t, r, s0, s1); });
+      const Place p = place(ent, tile);
+      each_sum([&](int t, int r, float s0, float s1) { emit(p, t, r, s0, s1); });
       clear();
     } else {
       open = true;
@@ -675,7 +693,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   if (kKind == kMvDown && len == 0) {  // no expert was hit: zeros
     const int n = mine * kMvRows * a.T;
     for (int o = threadIdx.x; o < n; o += kMvThreads)
-      emit(u0 + o / (kMvRows * a.T), o / kMvRows % a.T, o % kMvRows, 0.f, 0.f);
+      emit(place(0, u0 + o / (kMvRows * a.T)), o / kMvRows % a.T, o % kMvRows, 0.f, 0.f);
     return;
   }
   __syncthreads();
@@ -690,7 +708,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
         s0 += src[0];
         if constexpr (kDual) s1 += src[C::kTok * kMvRows];
       }
-      emit(u0, t, r, s0, s1);
+      int ent, tile;
+      locate(u0, ent, tile);
+      emit(place(ent, tile), t, r, s0, s1);
     }
     return;
   }
@@ -698,20 +718,28 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   static_assert(C::kRingTotal >= kMvWarps * C::kRed * 4, "the ring is large enough");
   if (open) put(red1 + warp * C::kRed);
   __syncthreads();
-  // A unit that is spread over warps: found at the first share that begins inside it; its sums are
-  // added in warp order.
-  for (int w = 1 + threadIdx.x / kOuts; w < kMvWarps; w += kMvThreads / kOuts) {
-    const int o = threadIdx.x % kOuts, r = o % kMvRows, t = o / kMvRows;
-    const int p = share(w), i = p / len, begin = i * len;
-    if (p == begin || p >= total || share(w - 1) > begin) continue;  // no unit begins its spread here
-    float s0 = 0.f, s1 = 0.f;
-    for (int k = w - 1; k < kMvWarps && share(k) < begin + len; ++k) {
+  // A unit that is spread over warps: the warp whose share is the first to begin inside it adds its sums
+  // in warp order. They are in `red1` of the warp before, then in `red` of each warp until its end.
+  const int i = first / max(len, 1), begin = i * len;
+  if (warp == 0 || first == begin || first >= total || share(warp - 1) > begin) return;
+  int last = warp;
+  while (last + 1 < kMvWarps && share(last + 1) < begin + len) ++last;
+  int ent, tile;
+  locate(u0 + i, ent, tile);
+  const Place p = place(ent, tile);
+#pragma unroll
+  for (int o = lane; o < kOuts; o += 32) {
+    const int r = o % kMvRows, t = o / kMvRows;
+    const float* src = red1 + (warp - 1) * C::kRed + red_at(t, r);
+    float s0 = src[0], s1 = 0.f;
+    if constexpr (kDual) s1 = src[C::kTok * kMvRows];
+    for (int k = warp; k <= last; ++k) {
       if (share(k) == share(k + 1)) continue;  // nothing
-      const float* src = (share(k) > begin ? red : red1) + k * C::kRed + red_at(t, r);
+      src = red + k * C::kRed + red_at(t, r);
       s0 += src[0];
       if constexpr (kDual) s1 += src[C::kTok * kMvRows];
     }
-    emit(u0 + i, t, r, s0, s1);
+    emit(p, t, r, s0, s1);
   }
 }
 
