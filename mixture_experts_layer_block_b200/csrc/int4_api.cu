@@ -19,8 +19,8 @@ namespace {
 int check_format(int64_t rows, int64_t cols, int32_t group) {
   if (rows < 1 || cols < 8 || cols % 8 != 0) return MOE_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return MOE_ERR_INVALID_ARG;
-  // row tiles and column indices stay within 31 bits
-  if (rows > ((int64_t)1 << 34) || cols > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  // row tiles, column indices and the blocks of a CTA's share stay within 28 bits
+  if (cols > (1 << 24) || rows > ((int64_t)1 << 42) / cols) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -18,6 +18,7 @@
 // inputs give equal bits.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "ffn.cuh"
 #include "launch.h"
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   const int mine = each + ((int)blockIdx.x < more ? 1 : 0);
   const int len = kKind == kMvDown ? nhit * nb + shared * snb : nb;
   const int total = mine * len;
-  auto share = [&](int w) { return (int)((uint64_t)w * (uint32_t)total / kMvWarps); };  // where warp w's begins
+  auto share = [&](int w) { return (int)((uint32_t)(w * total) / kMvWarps); };  // where warp w's begins
 
   auto locate = [&](int u, int& ent, int& tile) {  // a unit's matrix (kMvDown: the first) and tile
     ent = 0;
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     const int o = threadIdx.x, r = o % kMvRows, t = o / kMvRows;
     if (o < kOuts) {
       float s0 = 0.f, s1 = 0.f;
-#pragma unroll
+#pragma unroll 4
       for (int w = 0; w < kMvWarps; ++w) {
         const float* src = red + w * C::kRed + red_at(t, r);
         s0 += src[0];
@@ -718,28 +719,31 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   static_assert(C::kRingTotal >= kMvWarps * C::kRed * 4, "the ring is large enough");
   if (open) put(red1 + warp * C::kRed);
   __syncthreads();
-  // A unit that is spread over warps: the warp whose share is the first to begin inside it adds its sums
-  // in warp order. They are in `red1` of the warp before, then in `red` of each warp until its end.
-  const int i = first / max(len, 1), begin = i * len;
-  if (warp == 0 || first == begin || first >= total || share(warp - 1) > begin) return;
-  int last = warp;
-  while (last + 1 < kMvWarps && share(last + 1) < begin + len) ++last;
-  int ent, tile;
-  locate(u0 + i, ent, tile);
-  const Place p = place(ent, tile);
-#pragma unroll
-  for (int o = lane; o < kOuts; o += 32) {
-    const int r = o % kMvRows, t = o / kMvRows;
-    const float* src = red1 + (warp - 1) * C::kRed + red_at(t, r);
+  // Units that are spread over warps, a thread to an output. Lane w looks at share w: a unit is spread
+  // where a share is the first to begin inside it. Its sums are in `red1` of the warp before and in `red`
+  // of each warp until its end, and are added in warp order.
+  const int mark = lane <= kMvWarps ? share(lane) : INT_MAX;  // where share `lane` begins
+  const int before = __shfl_up_sync(0xffffffffu, mark, 1), after = __shfl_down_sync(0xffffffffu, mark, 1);
+  const int at = lane > 0 && lane < kMvWarps && mark < total ? mark / len : -1;
+  const uint32_t firsts = __ballot_sync(0xffffffffu, at >= 0 && mark > at * len && before <= at * len);
+  for (int item = threadIdx.x; item < __popc(firsts) * kOuts; item += kMvThreads) {  // whole warps
+    uint32_t m = firsts;
+    for (int j = item / kOuts; j > 0; --j) m &= m - 1;
+    const int w = __ffs(m) - 1, i = __shfl_sync(0xffffffffu, at, w);
+    uint32_t spread = __ballot_sync(0xffffffffu, lane >= w && lane < kMvWarps && mark < (i + 1) * len && mark != after);
+    const int o = item % kOuts, r = o % kMvRows, t = o / kMvRows;
+    const float* src = red1 + (w - 1) * C::kRed + red_at(t, r);
     float s0 = src[0], s1 = 0.f;
     if constexpr (kDual) s1 = src[C::kTok * kMvRows];
-    for (int k = warp; k <= last; ++k) {
-      if (share(k) == share(k + 1)) continue;  // nothing
-      src = red + k * C::kRed + red_at(t, r);
-      s0 += src[0];
-      if constexpr (kDual) s1 += src[C::kTok * kMvRows];
+    src = red + red_at(t, r);
+    for (; spread; spread &= spread - 1) {
+      const float* k = src + (__ffs(spread) - 1) * C::kRed;
+      s0 += k[0];
+      if constexpr (kDual) s1 += k[C::kTok * kMvRows];
     }
-    emit(p, t, r, s0, s1);
+    int ent, tile;
+    locate(u0 + i, ent, tile);
+    emit(place(ent, tile), t, r, s0, s1);
   }
 }
 
