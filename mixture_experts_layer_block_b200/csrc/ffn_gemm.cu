@@ -142,12 +142,14 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_go = reinterpret_cast<volatile int*>(s_tmem + 2);           // [2]
   volatile uint32_t* s_nfill = reinterpret_cast<volatile uint32_t*>(s_tmem + 4);  // [4] fills per producer
+  volatile uint32_t* s_left = reinterpret_cast<volatile uint32_t*>(s_tmem + 8);   // a role of the pair gave up
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   DeviceMeta* meta = P.meta;
   const int64_t limit = P.timeout_ns;
+  const int64_t drain_limit = max(limit, (int64_t)2000000000);  // copies in flight are waited for whatever the limit
   // one ring for the whole launch: its stage holds the largest product's operands
   int stage_bytes = 0;
   for (int i = 0; i < P.nprob; ++i) stage_bytes = max(stage_bytes, kFABytes + b_bytes(P.p[i].bn, P.p[i].b_mn));
@@ -172,6 +174,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     mbar_init(drain, 1);
     *s_abort = 0;
     for (int i = 0; i < 4; ++i) s_nfill[i] = 0;
+    *s_left = 0;
     fence_mbar_init();
     for (int i = 0; i < P.nprob; ++i) {
       tma_prefetch_desc(&P.p[i].a[0]);
@@ -189,6 +192,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   griddep_wait();
   const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
   const uint32_t acc_empty_c0 = mapa_shared(smem_u32(acc_empty), 0);
+  const uint32_t left_c0 = mapa_shared(smem_u32((const void*)s_left), 0);
   uint32_t nfill = 0;
   bool mma_issued = false;
 
@@ -253,7 +257,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         const uint32_t idesc = idesc_bf16_f32(kFfnTileM, p.bn) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
         // a 16-wide K step: 32 bytes further along a K-major row, two atoms along MN-major k
         const uint64_t astep = p.a_mn ? (2048 >> 4) : (32 >> 4), bstep = p.b_mn ? (2048 >> 4) : (32 >> 4);
-        if (!wait_bar(&acc_empty[acc], acc_phase ^ 1, meta, s_abort, limit, kSiteMmaAcc)) break;
+        if (!wait_bar_fast(&acc_empty[acc], acc_phase ^ 1, meta, s_abort, limit, kSiteMmaAcc)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * kAccCols;
         for (int kb = k0; kb < k1; ++kb) {
@@ -273,6 +280,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         umma_commit_pair_mc(&acc_full[acc], 3);
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
+      if (!ok) *s_left = 1;
     }
     __syncwarp();
   } else if (warp == 7) {
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       }
       bulk_wait_group<0>();
       for (uint32_t b = 0; b < 2; ++b)  // after an abort, loads that nobody waited for
-        if (loads > b) wait_bar_drain(&ug_full[b], (((loads - 1 - b) >> 1)) & 1, meta, limit);
+        if (loads > b) wait_bar_drain(&ug_full[b], ((loads - 1 - b) >> 1) & 1, meta, drain_limit);
     }
     __syncwarp();
   } else {
@@ -368,7 +376,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       // leave the loop together
       if (leader) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
       named_bar_sync(1, 128);
-      if (s_go[it & 1] == 0) break;
+      if (s_go[it & 1] == 0) {
+        if (leader) st_cluster_u32(left_c0, 1);
+        break;
+      }
       tc_fence_after();
       const uint32_t tacc = tmem_base + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
       const int mstore = p.splits > 1 ? t.split * p.mpad + m0 : m0;
@@ -503,24 +514,28 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   }
 
   griddep_launch_dependents();
-  // teardown: every fill of either CTA completes on CTA 0's `full` barriers, and every MMA writes
-  // both CTAs' tensor memory, so CTA 0 drains both before either CTA moves on
+  // teardown. Where every unit was finished, every fill was consumed and every MMA waited for (by both
+  // epilogues): nothing is in flight. After an abort CTA 0 drains both CTAs' fills, which complete on its
+  // `full` barriers, and the MMAs, which write both CTAs' tensor memory, before either CTA moves on.
+  // (Draining always took 3 us of every launch.)
   tc_fence_before();
   if (lane == 0 && (warp == 0 || warp == 6))
     st_cluster_u32(mapa_shared(smem_u32((const void*)&s_nfill[2 * rank + (warp == 6 ? 1 : 0)]), 0), nfill);
   cluster_sync_all();
-  if (rank == 0 && threadIdx.x == 0) {
-    // after an abort some producers may have issued up to a ring's worth of fills that others did
-    // not: arrive for those so that the phases complete when the bytes land
-    uint32_t hi = 0;
-    for (int i = 0; i < 4; ++i) hi = max(hi, s_nfill[i]);
-    for (int i = 0; i < 4; ++i)
-      for (uint32_t j = s_nfill[i]; j < hi; ++j) mbar_arrive(&full[j % nst]);
-    drain_fills(full, nst, hi, meta, limit);
-  }
-  if (mma_issued) {  // in the thread that issued the MMAs
-    umma_commit_pair(drain);
-    wait_bar_drain(drain, 0, meta, limit);
+  if (rank == 0 && *s_left) {
+    if (threadIdx.x == 0) {
+      // some producers may have issued up to a ring's worth of fills that others did not: arrive for
+      // those so that the phases complete when the bytes land
+      uint32_t hi = 0;
+      for (int i = 0; i < 4; ++i) hi = max(hi, s_nfill[i]);
+      for (int i = 0; i < 4; ++i)
+        for (uint32_t j = s_nfill[i]; j < hi; ++j) mbar_arrive(&full[j % nst]);
+      drain_fills(full, nst, hi, meta, drain_limit);
+    }
+    if (mma_issued) {  // in the thread that issued the MMAs
+      umma_commit_pair(drain);
+      wait_bar_drain(drain, 0, meta, drain_limit);
+    }
   }
   cluster_sync_all();
   tc_fence_after();
