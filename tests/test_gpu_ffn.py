@@ -83,7 +83,9 @@ def _close(got, ref, err, name):
 
 # one token to several m-tiles; sizes off every tile, chunk and 64-wide block; the smallest sizes
 SHAPES = [(1, 256, 128), (5, 264, 136), (16, 2048, 512), (17, 264, 136), (31, 8, 8), (64, 1024, 72), (127, 72, 1024),
-          (128, 512, 256), (129, 2048, 512), (257, 328, 1032), (333, 2048, 200), (515, 2048, 512), (1030, 520, 1544)]
+          (128, 512, 256), (129, 2048, 512), (257, 328, 1032), (333, 2048, 200), (515, 2048, 512), (1030, 520, 1544),
+          # few tokens and long sums over few tiles
+          (5, 264, 2048), (16, 2568, 2048), (9, 24, 4104)]
 
 
 @pytest.mark.parametrize("T,H,D", SHAPES)

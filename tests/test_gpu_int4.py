@@ -184,7 +184,9 @@ def _reference(x, ids, w, val, H, D, E, Ds):
 
 
 CASES = [(1, 256, 128, 8, 2, 0, 128, False), (16, 256, 128, 8, 2, 64, 32, True), (7, 272, 48, 5, 3, 0, 64, False),
-         (16, 528, 272, 300, 8, 144, 128, True), (9, 1024, 512, 32, 32, 0, 32, False), (8, 64, 1040, 3, 1, 0, 64, True)]
+         (16, 528, 272, 300, 8, 144, 128, True), (9, 1024, 512, 32, 32, 0, 32, False), (8, 64, 1040, 3, 1, 0, 64, True),
+         # long sums of few output tiles; more tiles than SMs, unevenly; every expert with more than 8 tokens
+         (16, 272, 1040, 8, 8, 0, 64, False), (16, 2560, 512, 24, 8, 272, 128, True), (7, 4816, 528, 16, 16, 0, 32, False)]
 
 
 @pytest.mark.parametrize("T,H,D,E,k,Ds,group,zeros", CASES)
