@@ -189,10 +189,13 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
-  griddep_wait();
+  // each role waits for the kernel in front (griddep_wait) where it first touches memory: finding its first
+  // unit, and fetching the code that does, goes before
   const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
   const uint32_t acc_empty_c0 = mapa_shared(smem_u32(acc_empty), 0);
-  const uint32_t left_c0 = mapa_shared(smem_u32((const void*)s_left), 0);
+  auto give_up = [&]() {  // known to both CTAs behind the teardown's barrier
+    for (uint32_t r = 0; r < 2; ++r) st_cluster_u32(mapa_shared(smem_u32((const void*)s_left), r), 1);
+  };
   uint32_t nfill = 0;
   bool mma_issued = false;
 
@@ -221,6 +224,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         int left = p.nkb * (seg + 1) - k0;
         int k = (k0 - seg * p.nkb) * kBK;
         const CUtensorMap* map = &maps[!is_a && p.b_by_rank ? (int)rank : seg];
+        if (nfill == 0) griddep_wait();
         for (int n = k1 - k0; n > 0; --n) {
           if (!wait_bar_fast(&empty[stage], phase ^ 1, meta, s_abort, limit, kSiteProducerEmpty)) { ok = false; break; }
           const uint32_t dst = ring + stage * stage_bytes;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         umma_commit_pair_mc(&acc_full[acc], 3);
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
-      if (!ok) *s_left = 1;
+      if (!ok) give_up();
     }
     __syncwarp();
   } else if (warp == 7) {
@@ -305,6 +309,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       };
       place(in);
       place(out);
+      griddep_wait();
       uint32_t loads = 0;
       auto load = [&]() {  // the next chunk's u and g into buffer loads % 2, which is free
         const uint32_t b = loads & 1;
@@ -367,6 +372,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         *reinterpret_cast<uint4*>(buf + row * 128 + ((j ^ (row & 7)) << 4)) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     };
+    griddep_wait();
     uint32_t it = 0;
     for (int id = pair; id < P.units; id += npairs, ++it) {
       const Unit t = find_unit_ffn(P, id);
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       if (leader) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
       named_bar_sync(1, 128);
       if (s_go[it & 1] == 0) {
-        if (leader) st_cluster_u32(left_c0, 1);
+        if (leader) give_up();
         break;
       }
       tc_fence_after();
@@ -522,8 +528,8 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   if (lane == 0 && (warp == 0 || warp == 6))
     st_cluster_u32(mapa_shared(smem_u32((const void*)&s_nfill[2 * rank + (warp == 6 ? 1 : 0)]), 0), nfill);
   cluster_sync_all();
-  if (rank == 0 && *s_left) {
-    if (threadIdx.x == 0) {
+  if (*s_left) {
+    if (rank == 0 && threadIdx.x == 0) {
       // some producers may have issued up to a ring's worth of fills that others did not: arrive for
       // those so that the phases complete when the bytes land
       uint32_t hi = 0;
@@ -536,8 +542,9 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       umma_commit_pair(drain);
       wait_bar_drain(drain, 0, meta, drain_limit);
     }
+    __syncwarp();
+    cluster_sync_all();
   }
-  cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * kAccCols);
 }
