@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * C::kStage * C::kDepth) + (uint32_t)lane * 16;
   const uint8_t* ring_p = smem + (size_t)warp * C::kStage * C::kDepth;
 
-  if (!a.early) griddep_wait();
+  if (kKind != kMvOne && !a.early) griddep_wait();  // the ids; one matrix: before its first copy
   int nhit = 1;
   if constexpr (kKind != kMvOne) {
     build_hits(a, hits, reinterpret_cast<uint32_t*>(red));  // the sums' buffer is free until the first unit
@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   Walk cur = prod;
   nxt = prod;
   aim_weights();
+  if (kKind == kMvOne && !a.early) griddep_wait();
   uint32_t slot = 0, vacant = 0;  // byte offsets in the ring: the block in use, the one used before it
 #pragma unroll 1
   for (int i = 0; i < C::kDepth - 1; ++i) {
