@@ -240,16 +240,15 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   if (!w || !w->up || !w->gate || !w->down || (u == nullptr) != (g == nullptr)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!x || !out || !workspace)) return MOE_ERR_INVALID_ARG;
   if (!all_aligned({x, w->up, w->gate, w->down, out, u, g, workspace})) return MOE_ERR_MISALIGNED;
-  if (workspace_bytes < moe_ffn_workspace_bytes(T, hidden, inter, 0)) return MOE_ERR_INVALID_ARG;
-  if (!h) return MOE_ERR_INVALID_ARG;
+  const int64_t H = hidden, D = inter;
+  const ForwardPlan f = T > 0 ? plan_forward(T, H, D) : ForwardPlan{};
+  if (workspace_bytes < f.bytes || !h) return MOE_ERR_INVALID_ARG;
   if (h->ffn_pairs < 1) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   h->last_stream = st;
-  const int64_t H = hidden, D = inter;
-  const ForwardPlan f = plan_forward(T, H, D);
   char* ws = static_cast<char*>(workspace);
   void* hb = ws + f.h;
 
@@ -325,14 +324,14 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   const moe_ffn_grads gr = grads ? *grads : none;
   if (!all_aligned({dout, x, u, g, w->up, w->gate, w->down, dx, gr.up, gr.gate, gr.down, workspace}))
     return MOE_ERR_MISALIGNED;
-  if (workspace_bytes < moe_ffn_workspace_bytes(T, hidden, inter, 1)) return MOE_ERR_INVALID_ARG;
-  if (!h) return MOE_ERR_INVALID_ARG;
+  const int64_t H = hidden, D = inter;
+  const BackwardPlan b = T > 0 ? plan_backward(T, H, D) : BackwardPlan{};
+  if (workspace_bytes < b.bytes || !h) return MOE_ERR_INVALID_ARG;
   if (h->ffn_pairs < 1) return MOE_ERR_UNSUPPORTED;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   h->last_stream = st;
-  const int64_t H = hidden, D = inter;
   void* dw[3] = {gr.up, gr.gate, gr.down};
   const int wkind = (flags & MOE_FFN_GRAD_ADD) ? 2 : ((flags & MOE_FFN_GRAD_F32) ? 1 : 0);
   if (T == 0) {  // sums over no tokens
@@ -341,7 +340,6 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
     return MOE_OK;
   }
   if (!dx && !dw[0] && !dw[1] && !dw[2]) return MOE_OK;
-  const BackwardPlan b = plan_backward(T, H, D);
   char* ws = static_cast<char*>(workspace);
   void *du = ws + b.du, *dg = ws + b.dg, *hb = ws + b.h;
 

@@ -8,6 +8,7 @@ is missing this module raises on import.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -432,20 +433,22 @@ class MoELayer:
         _is_tensor(down, "Ws_down", (H, D), _BF16, dev)
         return T, H, D, moe_shared_w(up.data_ptr(), gate.data_ptr(), down.data_ptr())
 
-    def _ffn_workspace(self, workspace, need, stream):
-        """The caller's workspace, or one for this call alone (allocated in the order of the
-        call's stream, so that its memory is reused only behind the call)."""
+    def _ffn_workspace(self, workspace, need, x, stream):
+        """Address and bytes of the caller's workspace, or of one for this call alone (allocated in the
+        order of the call's stream, so that its memory is reused only behind the call); and its owner."""
         if workspace is not None:
             _is_tensor(workspace, "workspace", getattr(workspace, "shape", None), _U8, self.device)
             if workspace.numel() < need:
                 raise ValueError(f"the workspace needs {need} bytes, got {workspace.numel()}")
-            return workspace
-        if stream is None:
-            return torch.empty(need, dtype=torch.uint8, device=self._torch_device)
-        with torch.cuda.stream(stream):
-            return torch.empty(need, dtype=torch.uint8, device=self._torch_device)
+        elif stream is None:
+            workspace = x.new_empty(need >> 1)  # of x's 2-byte type: the cheapest allocation there is
+        else:
+            with torch.cuda.stream(stream):
+                workspace = x.new_empty(need >> 1)
+        return workspace.data_ptr(), workspace.nbytes, workspace
 
     @staticmethod
+    @functools.lru_cache(maxsize=4096)
     def ffn_workspace_bytes(T, hidden, inter, backward=False):
         """Bytes of the workspace of ffn_forward or ffn_backward (a uint8 tensor)."""
         n = lib.moe_ffn_workspace_bytes(T, hidden, inter, 1 if backward else 0)
@@ -465,9 +468,9 @@ class MoELayer:
                 raise ValueError("u and g go together")
             _is_tensor(u, "u", (T, D), _BF16, self.device)
             _is_tensor(g, "g", (T, D), _BF16, self.device)
-        ws = self._ffn_workspace(workspace, self.ffn_workspace_bytes(T, H, D), stream)
+        ws, nbytes, owner = self._ffn_workspace(workspace, self.ffn_workspace_bytes(T, H, D), x, stream)
         check(lib.moe_ffn_forward(self.h, x.data_ptr(), T, H, D, w, out.data_ptr(), 1 if out.element_size() == 2 else 0,
-                                  _addr(u), _addr(g), ws.data_ptr(), ws.numel(), _raw_stream(stream, self.device)),
+                                  _addr(u), _addr(g), ws, nbytes, _raw_stream(stream, self.device)),
               "moe_ffn_forward")
         return out
 
@@ -495,10 +498,9 @@ class MoELayer:
                     raise TypeError("the weight gradients must all be bfloat16 or all float32")
             addr.append(_addr(t))
         flags = 0 if first is None or first.element_size() == 2 else MOE_FFN_GRAD_F32 | (MOE_FFN_GRAD_ADD if accumulate else 0)
-        ws = self._ffn_workspace(workspace, self.ffn_workspace_bytes(T, H, D, True), stream)
+        ws, nbytes, owner = self._ffn_workspace(workspace, self.ffn_workspace_bytes(T, H, D, True), x, stream)
         check(lib.moe_ffn_backward(self.h, dout.data_ptr(), x.data_ptr(), u.data_ptr(), g.data_ptr(), T, H, D, w,
-                                   _addr(dx), moe_ffn_grads(*addr), flags, ws.data_ptr(), ws.numel(),
-                                   _raw_stream(stream, dev)), "moe_ffn_backward")
+                                   _addr(dx), moe_ffn_grads(*addr), flags, ws, nbytes, _raw_stream(stream, dev)), "moe_ffn_backward")
         return grads
 
     # ---- MXFP8 experts ----
