@@ -13,9 +13,13 @@
 //    written back to shared memory, for products that take a fraction of the copy's time anyway;
 //  - 4-bit codes become bf16 exactly: (code | 0x4300) is 128 + code, less bf16(128 + zero). A group's
 //    sum is scaled in fp32, so nothing is rounded before the result;
-//  - a kernel behind another of the same call starts copying weights before that one is done.
+//  - a kernel behind another of the same call may copy weights before that one is done.
 // The sums of a unit that several warps share meet in shared memory and are added in warp order: equal
 // inputs give equal bits.
+// Measured (one B200, calls back to back on three sets of weights): W of 151552 x 4096 in 4 bits times one
+// token 80 us, 4.0 TB/s, bound by the integer pipe (unpacking 8 codes takes 7 of its half-rate operations:
+// with the shifts left out, and wrong numbers, 4.5 TB/s); 2048 x 7168 times one token 5.0 us, which is
+// latency: about 1.2 us to set up, 1 us to the first data, 0.3 us for the sums, and the change of kernels.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -79,7 +83,7 @@ struct Hits {
   uint8_t token[kMvMaxSlots];   // by pair
 };
 
-constexpr int kMvWarps = 16;  // one CTA to an SM
+constexpr int kMvWarps = 16;  // one CTA to an SM (20 warps, with fewer registers each, were within 5 % either way)
 constexpr int kMvThreads = kMvWarps * 32;
 
 // kGroup: columns to a scale, 0 for bf16 weights.
