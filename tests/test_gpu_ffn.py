@@ -85,7 +85,7 @@ def _close(got, ref, err, name):
 SHAPES = [(1, 256, 128), (5, 264, 136), (16, 2048, 512), (17, 264, 136), (31, 8, 8), (64, 1024, 72), (127, 72, 1024),
           (128, 512, 256), (129, 2048, 512), (257, 328, 1032), (333, 2048, 200), (515, 2048, 512), (1030, 520, 1544),
           # few tokens and long sums over few tiles
-          (5, 264, 2048), (16, 2568, 2048), (9, 24, 4104)]
+          (5, 264, 2048), (16, 2568, 2048), (9, 24, 4104), (2, 8, 8)]
 
 
 @pytest.mark.parametrize("T,H,D", SHAPES)
@@ -307,4 +307,73 @@ def test_matches_the_layers_shared_expert():
     _close(block, ref, eo, "block")
     err = eo + R16 * (ref.abs() + eo)
     assert bool(((whole.double() - ref).abs() <= err).all())
+    layer.close()
+
+
+def test_two_streams_at_once():
+    """Calls of one handle on two streams overlap, each with a workspace of its own, and agree with the
+    same calls one after another."""
+    layer = _layer()
+    cases = [(300, 520, 264), (12, 1024, 512)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    data, refs, got = [], [], []
+    for i, (T, H, D) in enumerate(cases):
+        x, wts, dout = _inputs(T, H, D, seed=30 + i)
+        u, g = (torch.empty(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ref = {"out": torch.empty_like(x), "x": torch.empty_like(x), **{n: torch.empty_like(w) for n, w in wts.items()}}
+        layer.ffn_forward(x, wts, ref["out"], u=u, g=g)
+        layer.ffn_backward(dout, x, u, g, wts, {n: v for n, v in ref.items() if n != "out"})
+        data.append((x, wts, dout, u, g))
+        refs.append(ref)
+        got.append([{n: torch.empty_like(v) for n, v in ref.items()} for _ in range(8)])
+    torch.cuda.synchronize()
+    for rep in range(8):
+        for i, st in enumerate(streams):
+            x, wts, dout, u, g = data[i]
+            layer.ffn_forward(x, wts, got[i][rep]["out"], stream=st)
+            layer.ffn_backward(dout, x, u, g, wts, {n: v for n, v in got[i][rep].items() if n != "out"}, stream=st)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for rep in range(8):
+            for n, v in refs[i].items():
+                assert torch.equal(got[i][rep][n], v), (i, rep, n)
+    assert layer.status() == (0, 0)
+    layer.close()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of x, out, dx and dout: rows at both ends against fp64, and the weight
+    gradients against fp64 sums over all rows."""
+    layer = _layer()
+    T, H, D = 5 * 2 ** 19 + 77, 1024, 64
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    _, wts, _ = _inputs(1, H, D, seed=3)
+    dout = torch.empty_like(x).normal_(generator=gen)
+    out, dx = torch.empty_like(x), torch.empty_like(x)
+    u, g = (torch.empty(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    layer.ffn_forward(x, wts, out, u=u, g=g)
+    grads = {"x": dx, "Ws_up": torch.empty(D, H, device="cuda")}
+    layer.ffn_backward(dout, x, u, g, wts, grads)
+    rows = torch.cat([torch.arange(0, 300), torch.arange(2 ** 21 - 200, 2 ** 21 + 200), torch.arange(T - 300, T)]).cuda()
+    ref, ru, rg, eo, eu, eg = _forward_reference(x[rows], wts)
+    _close(out[rows], ref, eo, "out")
+    _close(u[rows], ru, eu, "u")
+    _close(g[rows], rg, eg, "g")
+    back = _backward_reference(dout[rows], x[rows], u[rows], g[rows], wts)
+    _close(dx[rows], *back["x"], "x")
+    # W_up's gradient in slices; its fp32 sum of T products is off by at most T 2^-23 of their magnitudes'
+    dw, mag = (torch.zeros(D, H, dtype=torch.float64, device="cuda") for _ in range(2))
+    for r in range(0, T, 1 << 17):
+        c = slice(r, min(T, r + (1 << 17)))
+        uu, gg = u[c].double(), g[c].double()
+        s = torch.sigmoid(uu)
+        du = (dout[c].double() @ wts["Ws_down"].double()) * gg * (s * (1 + uu * (1 - s)))
+        dw += du.T @ x[c].double()
+        mag += du.abs().T @ x[c].double().abs()
+    assert bool(((grads["Ws_up"].double() - dw).abs() <= (R16 * 1.1 + T * R32) * mag).all())
+    # and closer on the whole: independent roundings of T terms (2^-8 each) leave about 2^-8 / sqrt(T) of
+    # the magnitudes' sum, and truncated additions a drift below 2^-12 of it
+    assert float((grads["Ws_up"].double() - dw).norm() / dw.norm()) < 0.02
+    assert layer.status() == (0, 0)
     layer.close()

@@ -186,7 +186,9 @@ def _reference(x, ids, w, val, H, D, E, Ds):
 CASES = [(1, 256, 128, 8, 2, 0, 128, False), (16, 256, 128, 8, 2, 64, 32, True), (7, 272, 48, 5, 3, 0, 64, False),
          (16, 528, 272, 300, 8, 144, 128, True), (9, 1024, 512, 32, 32, 0, 32, False), (8, 64, 1040, 3, 1, 0, 64, True),
          # long sums of few output tiles; more tiles than SMs, unevenly; every expert with more than 8 tokens
-         (16, 272, 1040, 8, 8, 0, 64, False), (16, 2560, 512, 24, 8, 272, 128, True), (7, 4816, 528, 16, 16, 0, 32, False)]
+         (16, 272, 1040, 8, 8, 0, 64, False), (16, 2560, 512, 24, 8, 272, 128, True), (7, 4816, 528, 16, 16, 0, 32, False),
+         # the smallest sizes
+         (1, 16, 16, 1, 1, 0, 32, True), (16, 16, 32, 2, 2, 16, 128, False)]
 
 
 @pytest.mark.parametrize("T,H,D,E,k,Ds,group,zeros", CASES)
@@ -390,4 +392,76 @@ def test_no_tokens():
     layer.matvec_int4(x, packed["W_up"], torch.empty(0, 8 * 128, device="cuda"))
     layer.experts_int4(x, torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda"), packed, out)
     layer.forward_int4(x, torch.zeros(8, 256, dtype=torch.bfloat16, device="cuda"), None, packed, out)
+    layer.close()
+
+
+def test_layer_forwards_beside_4_bit_calls():
+    """The bf16 forwards (fused and separate kernels) give the same bits before and after 4-bit calls of
+    the same handle, and the intermediates that those overwrite are not offered."""
+    from mixture_experts_layer_block_b200 import native
+    H, D, E, k, Ds = 256, 128, 8, 2, 64
+    g = torch.Generator().manual_seed(8)
+
+    def r(*shape, s=0.05):
+        return (torch.randn(shape, generator=g) * s).to(torch.bfloat16).cuda()
+
+    wts = {"W_router": r(E, H), "W_up": r(E, D, H), "W_gate": r(E, D, H), "W_down": r(E, H, D), "Ws_up": r(Ds, H),
+           "Ws_gate": r(Ds, H), "Ws_down": r(H, Ds)}
+    for flags in (0, native.MOE_FLAG_UNFUSED_SMALL):
+        layer = native.MoELayer(H, D, E, k, 16, 64, inter_shared=Ds, flags=flags)
+        wq = layer.quantize_experts_int4(wts, 32, True)
+        for T in (5, 16, 50):
+            x = r(T, H, s=1.0)
+            a, b, c = (torch.empty(T, H, device="cuda") for _ in range(3))
+            layer.forward(x, wts, a)
+            layer.debug_outputs(T, k, "cuda")
+            few = min(T, 16)
+            layer.forward_int4(x[:few].contiguous(), wts["W_router"], None, wq, c[:few])
+            with pytest.raises(native.MoEError) as err:
+                layer.debug_outputs(T, k, "cuda")
+            assert err.value.code == native.MOE_ERR_NOT_READY
+            layer.forward(x, wts, b)
+            assert torch.equal(a, b)
+            # 4-bit weights are near the bf16 ones: half a step of each (a 30th of a group's spread) leaves
+            # the layer's output well inside its own size
+            assert float((c[:few] - a[:few]).norm()) < 0.5 * float(a[:few].norm())
+        with pytest.raises(native.MoEError) as err:
+            layer.forward_int4(r(17, H), wts["W_router"], None, wq, torch.empty(17, H, device="cuda"))
+        assert err.value.code == native.MOE_ERR_UNSUPPORTED
+        assert layer.status() == (0, 0)
+        layer.close()
+
+
+def test_offsets_past_32_bits():
+    """Experts and rows whose codes lie more than 2^32 bytes into their buffers."""
+    H, D, E, k, T = 7168, 2048, 640, 2, 3  # 4.7 GB of codes a matrix
+    layer = _layer(H, D, E, k)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    packed, kept = {}, {}
+    some = [0, 300, 584, 638, 639]
+    for n, (R, K) in {"W_up": (E * D, H), "W_gate": (E * D, H), "W_down": (E * H, D)}.items():
+        q = torch.randint(0, 256, (R, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s = (torch.rand(R, K // 128, generator=g, device="cuda") + 0.5).mul(0.3 / K ** 0.5).to(torch.bfloat16)
+        packed[n] = layer.pack_int4(q, s, None, 128)
+        rows = R // E
+        kept[n] = {e: _values(torch.stack((q[e * rows:(e + 1) * rows] & 15, q[e * rows:(e + 1) * rows] >> 4), 2).flatten(1).cpu(),
+                              s[e * rows:(e + 1) * rows].cpu(), None, 128).cuda() for e in some}
+        del q, s
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.tensor([[0, 639], [638, 300], [584, 639]], dtype=torch.int32, device="cuda")
+    w = torch.rand(T, k, generator=g, device="cuda")
+    out = torch.empty(T, H, device="cuda")
+    layer.experts_int4(x, ids, w, packed, out)
+    for t in range(T):
+        ref, err = 0, 0
+        for j in range(k):
+            e, p = int(ids[t, j]), float(w[t, j])
+            y, ey = _block(x[t].double(), kept["W_up"][e], kept["W_gate"][e], kept["W_down"][e])
+            ref, err = ref + p * y, err + p * ey + 18 * R32 * p * y.abs()
+        _close(out[t], ref, err)
+    one = torch.empty(T, E * D, device="cuda")
+    layer.matvec_int4(x, packed["W_up"], one)
+    for e in some:
+        ref = x.double() @ kept["W_up"][e].T
+        _close(one[:, e * D:(e + 1) * D], ref, (H + 8) * R32 * (x.double().abs() @ kept["W_up"][e].abs().T))
     layer.close()
