@@ -288,7 +288,8 @@ MOE_API int64_t moe_int4_scale_bytes(int64_t rows, int64_t cols, int32_t group, 
 /* Quantise the device bf16 matrix src [rows][cols] (finite, magnitudes below 1e38), group by group
  * in fp32, to nearest even. Without zero points s = bf16(max|v| / 7), q = v / s + 8; with them
  * s = bf16((max - min) / 15), z = -min / s, q = v / s + z, where max and min also count 0; z and q
- * are clamped to 0..15. A group whose scale is 0 has q = z = 8. Any handle works. */
+ * are clamped to 0..15. A group whose scale is 0 has q = z = 8. Any handle works. This and the calls
+ * below refuse a result that overlaps another buffer of the call (MOE_ERR_INVALID_ARG). */
 MOE_API int moe_quantize_int4(moe_handle *h, const void *src, int64_t rows, int64_t cols, int32_t group,
                               int32_t zeros, void *codes, void *scales, void *stream);
 
@@ -301,8 +302,9 @@ MOE_API int moe_pack_int4(moe_handle *h, const uint8_t *q, const void *s, const 
                           int64_t cols, int32_t group, void *codes, void *scales, void *stream);
 
 /* out[t] = W x[t]: x device bf16 [T][cols], out device [T][rows], bf16 (out_bf16 = 1, rounded once)
- * or fp32 (on its own type's boundary: rows may be any number). Any handle works. Any T (0..2^24), but every 16 tokens are a launch that reads the
- * weights again. rows up to 2^31 - 1. No scratch memory: calls on different streams may overlap. */
+ * or fp32 (on its own type's boundary: rows may be any number). Any handle works. Any T (0..2^24),
+ * but every 16 tokens are a launch that reads the weights again. rows up to 2^31 - 1. No scratch
+ * memory: calls on different streams may overlap. */
 MOE_API int moe_matvec_int4(moe_handle *h, const void *x, int64_t T, const moe_int4_mat *w, int64_t rows,
                             int64_t cols, int32_t group, int32_t zeros, void *out, int32_t out_bf16,
                             void *stream);
@@ -340,8 +342,8 @@ MOE_API int moe_forward_int4(moe_handle *h, const void *x, int32_t T, const void
  * stays current. Products are summed in fp32 in a fixed order: equal inputs give equal bits.
  *   T       tokens, 0..2^24;  hidden H and inter D: multiples of 8, 8..2^20
  *   w       device bf16: up [D][H], gate [D][H], down [H][D]
- * Buffers must not overlap one another. MOE_ERR_INVALID_ARG for a null pointer, a bad size or a
- * workspace that is too small, MOE_ERR_UNSUPPORTED for sizes beyond those above (and on a device
+ * MOE_ERR_INVALID_ARG for a null pointer, a bad size, a workspace that is too small, and for a result
+ * or workspace that overlaps another buffer of the call (inputs may overlap one another), MOE_ERR_UNSUPPORTED for sizes beyond those above (and on a device
  * without room for a pair of SMs), MOE_ERR_MISALIGNED for a pointer off a 16-byte boundary. */
 
 /* Workspace bytes of moe_ffn_forward (backward = 0) or moe_ffn_backward (1); -1 for sizes that
@@ -385,8 +387,9 @@ MOE_API int moe_forward_host_join(moe_handle *h, void *stream, int32_t block);
  * *device_status = 0 when every kernel since the last call finished normally, else a
  * device error code (bit 30 set, low bits naming the wait that ran out). The word is
  * cleared by this call. It also covers the moe_ffn_* calls: after one of their waits ran out, the
- * handle's later ones give up at once, until this call has reported it. Returns MOE_ERR_DEVICE_TIMEOUT if a wait ran out, MOE_ERR_CUDA if
- * the stream reported a CUDA error, else MOE_OK. */
+ * handle's later ones give up at once, until this call has reported it. Returns
+ * MOE_ERR_DEVICE_TIMEOUT if a wait ran out, MOE_ERR_CUDA if the stream reported a CUDA error, else
+ * MOE_OK. */
 MOE_API int moe_get_status(moe_handle *h, int32_t *device_status);
 
 /* Stage entry points (each is one step of moe_forward, callable on its own).

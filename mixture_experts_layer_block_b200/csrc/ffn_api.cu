@@ -242,6 +242,10 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   if (!all_aligned({x, w->up, w->gate, w->down, out, u, g, workspace})) return MOE_ERR_MISALIGNED;
   const int64_t H = hidden, D = inter;
   const ForwardPlan f = T > 0 ? plan_forward(T, H, D) : ForwardPlan{};
+  const int64_t act = T * H * 2, pre = T * D * 2, wb = H * D * 2;
+  if (clobbers({{out, out_bf16 ? act : 2 * act}, {u, pre}, {g, pre}, {workspace, f.bytes}},
+               {{x, act}, {w->up, wb}, {w->gate, wb}, {w->down, wb}}))
+    return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < f.bytes || !h) return MOE_ERR_INVALID_ARG;
   if (h->ffn_pairs < 1) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -326,6 +330,10 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
     return MOE_ERR_MISALIGNED;
   const int64_t H = hidden, D = inter;
   const BackwardPlan b = T > 0 ? plan_backward(T, H, D) : BackwardPlan{};
+  const int64_t act = T * H * 2, pre = T * D * 2, wb = H * D * 2, gb = (flags & MOE_FFN_GRAD_F32) ? 2 * wb : wb;
+  if (clobbers({{dx, act}, {gr.up, gb}, {gr.gate, gb}, {gr.down, gb}, {workspace, b.bytes}},
+               {{dout, act}, {x, act}, {u, pre}, {g, pre}, {w->up, wb}, {w->gate, wb}, {w->down, wb}}))
+    return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < b.bytes || !h) return MOE_ERR_INVALID_ARG;
   if (h->ffn_pairs < 1) return MOE_ERR_UNSUPPORTED;
   DeviceScope dev(h->device);

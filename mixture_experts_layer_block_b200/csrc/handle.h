@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <vector>
 
 #include "launch.h"
@@ -111,6 +112,30 @@ inline int encode_map(moe_handle* h, CUtensorMap* out, const void* ptr, uint64_t
 inline int check_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 inline int select_device(moe_handle* h) { return check_cuda(cudaSetDevice(h->device)); }
+
+// A buffer of a call, to tell whether two of them overlap.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+
+inline bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes;
+}
+
+// Whether one of the buffers that a call writes overlaps another, or one that it reads: kernels read
+// and write tiles in no fixed order, so that the results would depend on timing.
+inline bool clobbers(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
+  for (const Span* w = writes.begin(); w != writes.end(); ++w) {
+    for (const Span* o = w + 1; o != writes.end(); ++o)
+      if (overlap(*w, *o)) return true;
+    for (const Span& r : reads)
+      if (overlap(*w, r)) return true;
+  }
+  return false;
+}
 
 // The handle's device for the length of one call; the caller's device is put back at the end.
 class DeviceScope {

@@ -102,6 +102,9 @@ int moe_quantize_int4(moe_handle* h, const void* src, int64_t rows, int64_t cols
   if ((rc = check_format(rows, cols, group))) return rc;
   if (!src || !codes || !scales) return MOE_ERR_INVALID_ARG;
   if (!aligned16(src) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_MISALIGNED;
+  if (clobbers({{codes, int4_code_bytes(rows, cols)}, {scales, int4_scale_bytes(rows, cols, group, zeros != 0)}},
+               {{src, rows * cols * 2}}))
+    return MOE_ERR_INVALID_ARG;
   if (!h) return MOE_ERR_INVALID_ARG;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
@@ -116,6 +119,10 @@ int moe_pack_int4(moe_handle* h, const uint8_t* q, const void* s, const uint8_t*
   if (!q || !s || !codes || !scales) return MOE_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(s) || !aligned16(z) || !aligned16(codes) || !aligned16(scales))
     return MOE_ERR_MISALIGNED;
+  const int64_t entries = rows * ((cols + group - 1) / group);
+  if (clobbers({{codes, int4_code_bytes(rows, cols)}, {scales, int4_scale_bytes(rows, cols, group, z != nullptr)}},
+               {{q, rows * cols / 2}, {s, entries * 2}, {z, entries}}))
+    return MOE_ERR_INVALID_ARG;
   if (!h) return MOE_ERR_INVALID_ARG;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
@@ -132,6 +139,11 @@ int moe_matvec_int4(moe_handle* h, const void* x, int64_t T, const moe_int4_mat*
   if (rows > INT32_MAX || T > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned(*w) || (reinterpret_cast<uintptr_t>(out) & (out_bf16 ? 1u : 3u)) != 0)
     return MOE_ERR_MISALIGNED;
+  if (clobbers({{out, T * rows * (out_bf16 ? 2 : 4)}},
+               {{x, T * cols * 2},
+                {w->codes, int4_code_bytes(rows, cols)},
+                {w->scales, int4_scale_bytes(rows, cols, group, zeros != 0)}}))
+    return MOE_ERR_INVALID_ARG;
   if (!h) return MOE_ERR_INVALID_ARG;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
@@ -157,6 +169,9 @@ int moe_experts_int4(moe_handle* h, const void* x, int32_t T, const int32_t* top
   if ((rc = check_experts(h, T, top_k, w))) return rc;
   if (T > 0 && (!x || !topk_ids || !topk_w || !out)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(out)) return MOE_ERR_MISALIGNED;
+  const int64_t n = (int64_t)T * h->cfg.hidden, slots = (int64_t)T * top_k;
+  if (clobbers({{out, n * (out_bf16 ? 2 : 4)}}, {{x, n * 2}, {topk_ids, slots * 4}, {topk_w, slots * 4}}))
+    return MOE_ERR_INVALID_ARG;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -173,6 +188,8 @@ int moe_forward_int4(moe_handle* h, const void* x, int32_t T, const void* w_rout
   if ((rc = check_experts(h, T, top_k, w))) return rc;
   if (!w_router || (T > 0 && (!x || !out))) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(out) || !aligned16(router_bias)) return MOE_ERR_MISALIGNED;
+  const int64_t n = (int64_t)T * h->cfg.hidden;
+  if (clobbers({{out, n * ((h->cfg.flags & MOE_FLAG_OUT_BF16) ? 2 : 4)}}, {{x, n * 2}})) return MOE_ERR_INVALID_ARG;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

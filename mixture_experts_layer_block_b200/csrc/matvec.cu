@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   int nhit = 1;
   if constexpr (kKind != kMvOne) {
     build_hits(a, hits, reinterpret_cast<uint32_t*>(red));  // the sums' buffer is free until the first unit
-    static_assert(kMvWarps * C::kRed * 4 >= hit_scratch(kNT * 8 * kMaxTopK), "its scratch memory fits");
+    constexpr int kSlots = kKind == kMvUp ? kMvMaxSlots : kNT * 8 * kMaxTopK;
+    static_assert(kMvWarps * C::kRed * 4 >= hit_scratch(kSlots), "its scratch memory fits");
     nhit = hits->n;
   }
 

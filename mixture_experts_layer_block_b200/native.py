@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -309,10 +310,13 @@ class MoELayer:
     # ---- 4-bit weights ----
     def quantize_int4(self, src, group=128, zeros=False, stream=None):
         """moe_quantize_int4 of a bf16 CUDA matrix [R, K] (a 3-D tensor is viewed as [-1, K])."""
-        m = src.reshape(-1, src.shape[-1])
-        _is_tensor(m, "src", m.shape, _BF16, self.device)
-        out = self._int4_matrix(m.shape[0], m.shape[1], group, zeros, stream)
-        check(lib.moe_quantize_int4(self.h, m.data_ptr(), out.rows, out.cols, group, 1 if zeros else 0, out.c.codes,
+        shape = getattr(src, "shape", ())
+        if len(shape) < 2:
+            raise ValueError("src must be a matrix or a stack of them")
+        # no copy is made of a strided tensor: nothing would order it with `stream`
+        _is_tensor(src, "src", shape, _BF16, self.device)
+        out = self._int4_matrix(math.prod(shape[:-1]), shape[-1], group, zeros, stream)
+        check(lib.moe_quantize_int4(self.h, src.data_ptr(), out.rows, out.cols, group, 1 if zeros else 0, out.c.codes,
                                     out.c.scales, _raw_stream(stream, self.device)), "moe_quantize_int4")
         return out
 

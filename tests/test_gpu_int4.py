@@ -188,7 +188,9 @@ CASES = [(1, 256, 128, 8, 2, 0, 128, False), (16, 256, 128, 8, 2, 64, 32, True),
          # long sums of few output tiles; more tiles than SMs, unevenly; every expert with more than 8 tokens
          (16, 272, 1040, 8, 8, 0, 64, False), (16, 2560, 512, 24, 8, 272, 128, True), (7, 4816, 528, 16, 16, 0, 32, False),
          # the smallest sizes
-         (1, 16, 16, 1, 1, 0, 32, True), (16, 16, 32, 2, 2, 16, 128, False)]
+         (1, 16, 16, 1, 1, 0, 32, True), (16, 16, 32, 2, 2, 16, 128, False),
+         # the most slots and experts
+         (16, 64, 32, 1024, 32, 16, 64, False), (8, 64, 32, 1024, 32, 0, 32, True)]
 
 
 @pytest.mark.parametrize("T,H,D,E,k,Ds,group,zeros", CASES)
@@ -464,4 +466,34 @@ def test_offsets_past_32_bits():
     for e in some:
         ref = x.double() @ kept["W_up"][e].T
         _close(one[:, e * D:(e + 1) * D], ref, (H + 8) * R32 * (x.double().abs() @ kept["W_up"][e].abs().T))
+    layer.close()
+
+
+def test_overlapping_results_are_refused():
+    from mixture_experts_layer_block_b200 import native
+    H, D, E, k, T = 64, 32, 4, 2, 8
+    layer = _layer(H, D, E, k)
+    _, packed = _experts(H, D, E, 0, 64, True, 5, layer)
+    buf = torch.randn(2 * T, H, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    x, ids = buf[:T], torch.tensor([[0, 1]] * T, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), 0.5, device="cuda")
+    router = torch.zeros(E, H, dtype=torch.bfloat16, device="cuda")
+    for out in (x, buf[1:T + 1], buf[T - 1:2 * T - 1]):
+        with pytest.raises(native.MoEError) as err:
+            layer.experts_int4(x, ids, w, packed, out)
+        assert err.value.code == native.MOE_ERR_INVALID_ARG
+    with pytest.raises(native.MoEError) as err:
+        layer.forward_int4(x, router, None, packed, buf.view(torch.float32).view(T, H))
+    assert err.value.code == native.MOE_ERR_INVALID_ARG
+    ref, out = torch.empty_like(x), buf[T:]
+    layer.experts_int4(x, ids, w, packed, ref)
+    layer.experts_int4(x, ids, w, packed, out)  # side by side is not overlapping
+    assert torch.equal(out, ref)
+    square = layer.quantize_int4(torch.randn(H, H, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda(), 64)
+    with pytest.raises(native.MoEError) as err:
+        layer.matvec_int4(x, square, x)
+    assert err.value.code == native.MOE_ERR_INVALID_ARG
+    layer.matvec_int4(x, square, out)
+    layer.matvec_int4(x, square, ref)
+    assert torch.equal(out, ref)
     layer.close()

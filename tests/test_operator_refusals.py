@@ -175,6 +175,11 @@ def test_binding_checks_int4_arguments(native):
         native.Int4Matrix(16, 64, 48, False, "cpu")
     with pytest.raises(ValueError):
         layer.pack_int4(torch.zeros(16, dtype=torch.uint8), _bf16(16, 1))
+    with pytest.raises(ValueError, match="contiguous"):
+        layer.quantize_int4(_bf16(64, 16).T)
+    for bad in (_bf16(64), 1.0):
+        with pytest.raises(ValueError, match="matrix"):
+            layer.quantize_int4(bad)
     m = native.Int4Matrix(4 * 32, 64, 32, False, "cpu")  # the buffers' sizes need no GPU
     assert m.codes.numel() == 8 * 1024 and m.scales.numel() == 8 * 4 * 32 and m.device == -1
     with pytest.raises(ValueError, match="cuda:0"):
