@@ -254,6 +254,12 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           if (++stage == (uint32_t)nst) { stage = 0; phase ^= 1; }
         }
       }
+      // the arrivals of CTA 0's commits on this CTA's `empty` barriers: the last of them are here before
+      // this CTA may end
+      for (int i = 0; is_a && ok && i < nst; ++i) {
+        ok = wait_bar_fast(&empty[stage], phase ^ 1, meta, s_abort, limit, kSiteProducerEmpty);
+        if (++stage == (uint32_t)nst) { stage = 0; phase ^= 1; }
+      }
     }
     __syncwarp();
     nfill = __reduce_max_sync(0xffffffffu, nfill);  // every lane: what the elected one counted
@@ -262,6 +268,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     if (rank == 0 && elect_one()) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
+      griddep_wait();  // the kernel in front is not on this one's clock
       for (int id = pair; ok && id < P.units; id += npairs) {
         const Unit t = find_unit_ffn(P, id);
         const FfnProblem& p = P.p[t.prob];

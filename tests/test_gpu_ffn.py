@@ -377,3 +377,96 @@ def test_offsets_past_32_bits():
     assert float((grads["Ws_up"].double() - dw).norm() / dw.norm()) < 0.02
     assert layer.status() == (0, 0)
     layer.close()
+
+
+@pytest.mark.parametrize("T", [8, 40])
+def test_overlapping_results_are_refused(T):
+    from mixture_experts_layer_block_b200 import native
+    H, D = 64, 64
+    layer = _layer()
+    x, wts, dout = _inputs(T, H, D, seed=2)
+    buf = torch.zeros(4 * T, D, dtype=torch.bfloat16, device="cuda")
+    u, g, out = buf[:T], buf[T:2 * T], buf[2 * T:3 * T]  # side by side: allowed
+    layer.ffn_forward(x, wts, out, u=u, g=g)
+    ref = torch.empty_like(x)
+    layer.ffn_forward(x, wts, ref)
+    assert torch.equal(out, ref)
+
+    def forward(out=out, u=u, g=g, ws=None):
+        layer.ffn_forward(x, wts, out, u=u, g=g, workspace=ws)
+
+    grads = {"x": torch.empty_like(x), **{n: torch.empty_like(w) for n, w in wts.items()}}
+
+    def backward(dout=dout, ws=None, **kw):
+        layer.ffn_backward(dout, x, u, g, wts, dict(grads, **kw), workspace=ws)
+
+    big = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    inside = big[:2 * T * H].view(torch.bfloat16).view(T, H)
+    for call in (lambda: forward(out=x), lambda: forward(u=u, g=u), lambda: forward(out=buf[T + 1:2 * T + 1]),
+                 lambda: forward(out=wts["Ws_up"][:T]), lambda: forward(out=inside, ws=big),
+                 lambda: backward(x=dout), lambda: backward(x=x), lambda: backward(x=u),
+                 lambda: backward(Ws_up=grads["Ws_gate"]), lambda: backward(Ws_down=wts["Ws_down"]),
+                 lambda: backward(x=inside, ws=big)):
+        with pytest.raises(native.MoEError) as err:
+            call()
+        assert err.value.code == native.MOE_ERR_INVALID_ARG
+    backward()
+    backward(dout=x)  # an input may serve twice
+    assert layer.status() == (0, 0)
+    layer.close()
+
+
+def test_a_long_kernel_in_front_is_not_on_the_clock():
+    """The waits' limit counts from the end of the kernel in front: behind one of about a millisecond
+    that lets its successor in early, a limit of 0.2 ms is enough for a small call."""
+    from mixture_experts_layer_block_b200.native import MoELayer
+    layer = MoELayer(256, 128, 8, 2, 16, 16, timeout_ns=200_000)
+    x, wts, dout = _inputs(40, 264, 136, seed=8)
+    u, g = (torch.empty(40, 136, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ref, out = torch.empty_like(x), torch.empty_like(x)
+    dx, dref = torch.empty_like(x), torch.empty_like(x)
+    layer.ffn_forward(x, wts, ref, u=u, g=g)
+    layer.ffn_backward(dout, x, u, g, wts, {"x": dref})
+    long = torch.zeros(1 << 18, 1 << 14, dtype=torch.bfloat16, device="cuda")  # 8 GB: more than 1 ms to read
+    assert layer.status() == (0, 0)
+    for _ in range(3):
+        layer.quantize_int4(long)
+        layer.ffn_forward(x, wts, out)
+        layer.quantize_int4(long)
+        layer.ffn_backward(dout, x, u, g, wts, {"x": dx})
+    assert layer.status() == (0, 0)
+    assert torch.equal(out, ref) and torch.equal(dx, dref)
+    layer.close()
+
+
+@pytest.mark.parametrize("what", ["up", "down", "dh", "gradients"])
+def test_a_wait_that_runs_out_is_reported(what):
+    """Sums so long that the epilogue's wait for the first tile (a quarter of a millisecond, or 35 us where
+    the 2048 blocks of a gradient's sum are split 16 ways) passes a limit of 5 us: the call drains what it had in
+    flight and returns, the status says so and is cleared, and the next call is right."""
+    from mixture_experts_layer_block_b200.native import MOE_ERR_DEVICE_TIMEOUT, MoELayer
+    # 74 tiles of one product, each one sum of 1024 blocks of 64 whose K is not split; dx of 2048 blocks
+    T, H, D = {"up": (37 * 256, 1 << 16, 256), "down": (37 * 256, 512, 1 << 16), "dh": (37 * 256, 1 << 16, 512),
+               "gradients": (37 * 256, 512, 1 << 16)}[what]
+    layer = MoELayer(256, 128, 8, 2, 16, 16, timeout_ns=5_000)
+    x, dout = (torch.zeros(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    u, g = (torch.zeros(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wts = {"Ws_up": torch.zeros(D, H, dtype=torch.bfloat16, device="cuda"),
+           "Ws_gate": torch.zeros(D, H, dtype=torch.bfloat16, device="cuda"),
+           "Ws_down": torch.zeros(H, D, dtype=torch.bfloat16, device="cuda")}
+    if what in ("up", "down"):
+        layer.ffn_forward(x, wts, dout)
+    else:
+        layer.ffn_backward(dout, x, u, g, wts, {"x": torch.empty_like(x), **{n: torch.empty_like(w) for n, w in wts.items()}})
+    rc, st = layer.status()
+    assert rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30)
+    assert layer.status() == (0, 0)
+    x, wts, _ = _inputs(20, 64, 64, seed=1)
+    out = torch.empty(20, 64, device="cuda")
+    patient = _layer()
+    patient.ffn_forward(x, wts, out)
+    assert patient.status() == (0, 0)
+    ref, _, _, eo, _, _ = _forward_reference(x, wts)
+    _close(out, ref, eo, "out")
+    layer.close()
+    patient.close()
