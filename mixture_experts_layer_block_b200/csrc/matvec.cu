@@ -17,8 +17,8 @@
 // The sums of a unit that several warps share meet in shared memory and are added in warp order: equal
 // inputs give equal bits.
 // Measured (one B200, calls back to back on three sets of weights): W of 151552 x 4096 in 4 bits times one
-// token 80 us, 4.0 TB/s, bound by the integer pipe (unpacking 8 codes takes 7 of its half-rate operations:
-// with the shifts left out, and wrong numbers, 4.5 TB/s); 2048 x 7168 times one token 5.0 us, which is
+// token 77 us, 4.1 TB/s, bound by the integer pipe (unpacking 8 codes takes 7 of its half-rate operations:
+// with the shifts left out, and wrong numbers, 12 % less time); 2048 x 7168 times one token 4.5 us, which is
 // latency: about 1.2 us to set up, 1 us to the first data, 0.3 us for the sums, and the change of kernels.
 #include <algorithm>
 #include <atomic>
@@ -32,7 +32,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kMvSmem = 227 * 1024;      // shared memory of an SM that CTAs can use
+// Shared memory of a CTA, but for rings of fewer than two blocks. What it leaves of an SM's 256 KB is L1, where the
+// activations are found again, and one or two blocks in flight a warp (16 to 64 KB an SM) are enough: with 227 KB the
+// experts took 42.4 us for 16 tokens where they now take 37.9, the block 23.1 us for 16 tokens instead of 21.5, and
+// one token times 37888 x 4096 in 4 bits 25.7 us instead of 22.6.
+constexpr int kMvSmem = 63 * 1024;
 constexpr int kMvMaxDepth = 12;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -102,10 +106,12 @@ struct Mv {
   static constexpr int kTok = kKind == kMvUp ? 8 : kNT * 8;          // columns of a unit's sums
   static constexpr int kRed = kMats * kTok * kMvRows;                // floats of a warp's partial sums
   static constexpr int kRest = kMvWarps * kRed * (int)sizeof(float) + (kKind != kMvOne ? (int)sizeof(Hits) : 0);
-  static constexpr int kDepth = std::min(kMvMaxDepth, (kMvSmem - 1024 - kRest) / (kMvWarps * kStage));
+  static constexpr int kDepth = std::max(2, std::min(kMvMaxDepth, (kMvSmem - 1024 - kRest) / (kMvWarps * kStage)));
   static constexpr int kRingTotal = kMvWarps * kStage * kDepth;
   static constexpr int kSmem = kRingTotal + kRest;
-  static_assert(kDepth >= 3, "two blocks in flight beside the one in use");
+  static_assert(kSmem <= 227 * 1024, "what a CTA can have");
+  // percent of an SM's shared memory (228 KB, 1 KB of each CTA for the system) that the kernel asks for
+  static constexpr int kCarveout = std::min(100, ((kSmem + 2047) / 1024 * 100 + 227) / 228);
 };
 
 // Where a warp is in its share of the CTA's K blocks. A segment is a run of blocks of one matrix within
@@ -447,9 +453,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
   float acc[C::kMats][C::kXT][4];   // of the current matrix
   float tot[kNT][4];             // kMvDown: router-weighted, over the experts so far
   uint4 xa[C::kXT][C::kVecs], xb[C::kXT][C::kVecs];  // halves of a block: first, second
-  // Half h of a block's products; 4-bit: one half holds kParts / 2 groups, or half of the one.
+  // Half h of a block's products; 4-bit: one half holds kParts / 2 groups, or half of the one. Calls
+  // reload(n, v) behind the last use of x[n][v] (4-bit).
   float part[C::kMats][C::kXT][4];  // 4-bit: sums of the current group, not scaled
-  auto products = [&](const uint8_t* st, const uint4 (&x)[C::kXT][C::kVecs], int h) {
+  auto products = [&](const uint8_t* st, uint4 (&x)[C::kXT][C::kVecs], int h, auto&& reload) {
 #pragma unroll
     for (int i = 0; i < C::kMats; ++i) {
       if constexpr (kW4) {
@@ -499,6 +506,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
               else if (j & 1) mma_bf16(p, f[jj], v.z, v.w);
               else mma_bf16(p, f[jj], v.x, v.y);
             }
+            if (i == C::kMats - 1) {
+#pragma unroll
+              for (int j = g * kWords + 1; j < (g + 1) * kWords; j += 2) reload(n, j >> 1);
+            }
             if (C::kParts >= 2 || h == 1) {
               acc[i][n][0] += s0 * p[0];
               acc[i][n][1] += s0 * p[1];
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
       }
     }
   };
-  // One block: the copy of a later one, activations half a block ahead, and its products. The lanes
+  // One block: the copy of a later one, activations ahead, and its products. The lanes
   // share a block's scales, so that the copy into the slot of the block before waits for them all.
   auto turn = [&]() {
     const uint32_t at = slot;
@@ -529,17 +540,19 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     if (slot == C::kStage * C::kDepth) slot = 0;
     return ring_p + at;
   };
+  auto keep = [](int, int) {};
   auto block = [&]() {
-    load_x(xb, 1);
+    if constexpr (!kW4) load_x(xb, 1);
     cp_async_wait<C::kDepth - 2>();
     __syncwarp();
     if (prod.n) copy(vacant);
     cp_async_commit();
     const uint8_t* st = turn();
-    products(st, xa, 0);
+    products(st, xa, 0, keep);
     advance_x();
     load_x(xa, 0);
-    products(st, xb, 1);
+    products(st, xb, 1, keep);
+    if constexpr (kW4) load_x(xb, 1);
   };
   // The same for `t` blocks at which no segment ends (neither this one nor that of the copies) and
   // whose following block is whole: nothing is asked in this loop.
@@ -550,29 +563,41 @@ __global__ void __launch_bounds__(kMvThreads, 1) mv_kernel(const __grid_constant
     xk -= t * C::kCols;
 #pragma unroll 1
     for (; t > 0; --t) {
+      auto load_b = [&](int n, int v) { xb[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs + v)); };
+      auto load_a = [&](int n, int v) { xa[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * v); };
+      if constexpr (kW4) {
 #pragma unroll
-      for (int n = 0; n < C::kXT; ++n) {
+        for (int n = 0; n < C::kXT; ++n) xp[n] += xstep[n];
+      } else {
 #pragma unroll
-        for (int v = 0; v < C::kVecs; ++v) xb[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * (C::kVecs + v));
+        for (int n = 0; n < C::kXT; ++n) load_b(n, 0);
       }
       cp_async_wait<C::kDepth - 2>();
       __syncwarp();
       copy_block(vacant);
       cp_async_commit();
       const uint8_t* st = turn();
-      products(st, xa, 0);
+      // 4-bit: every vector of activations is loaded again as soon as it is used, three quarters of a block ahead
+      // (experts, 8 tokens of 7168 x 2048: 183 -> 179 us, since h comes from L2). bf16, whose block is one
+      // vector a half, is faster with the loads in two bunches (16 tokens: 21.5 us instead of 22.2).
+      if constexpr (kW4) {
+        products(st, xa, 0, load_a);
+        products(st, xb, 1, load_b);
+      } else {
+        products(st, xa, 0, keep);
 #pragma unroll
-      for (int n = 0; n < C::kXT; ++n) {
-        xp[n] += xstep[n];
-#pragma unroll
-        for (int v = 0; v < C::kVecs; ++v) xa[n][v] = *reinterpret_cast<const uint4*>(xp[n] + 32 * v);
+        for (int n = 0; n < C::kXT; ++n) {
+          xp[n] += xstep[n];
+          load_a(n, 0);
+        }
+        products(st, xb, 1, keep);
       }
-      products(st, xb, 1);
     }
   };
 
   aim_x();
   load_x(xa, 0);
+  if constexpr (kW4) load_x(xb, 1);
   // Where a unit's results go: column or token t's row is row0 + t, for t < count; output rows below R.
   struct Place {
     int64_t row0;
@@ -759,8 +784,8 @@ template <bool kDual, int kKind, int kNT, int kGroup, bool kZeros>
 cudaError_t launch_mv(const MvArgs& a, int64_t units, int num_sms, cudaStream_t stream) {
   using C = Mv<kDual, kKind, kNT, kGroup, kZeros>;
   auto* k = mv_kernel<kDual, kKind, kNT, kGroup, kZeros>;
-  // the kernel's shared-memory limit is raised at its first launch on a device; should the device have
-  // been reset since, the launch is refused once and repeated
+  // the kernel's shared-memory limit and share are set at its first launch on a device; should the device
+  // have been reset since, the launch is refused once and repeated
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -770,6 +795,7 @@ cudaError_t launch_mv(const MvArgs& a, int64_t units, int num_sms, cudaStream_t 
   for (int attempt = 0;; ++attempt) {
     if (attempt > 0 || !(raised.load(std::memory_order_relaxed) & bit)) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, C::kCarveout);
       if (e != cudaSuccess) return e;
       raised.fetch_or(bit, std::memory_order_relaxed);
     }
