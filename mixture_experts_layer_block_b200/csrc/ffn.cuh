@@ -16,7 +16,7 @@
 
 namespace moe {
 
-constexpr int kFfnTileM = 256;   // rows of an output tile (128 per CTA of a pair)
+constexpr int kFfnTileM = 256;   // rows of the MMA, and the most of an output tile (128 per CTA of a pair)
 constexpr int kFfnMaxBN = 256;   // most columns of an output tile
 constexpr int kFfnMaxProblems = 4;
 constexpr int kFfnRaster = 8;    // m-tiles walked side by side, so that their B tiles stay in L2
@@ -27,12 +27,13 @@ struct alignas(64) FfnProblem {
                            // b[r] is what CTA r of the pair stages (W_up rows | W_gate rows)
   CUtensorMap out;         // bf16 or fp32 [M][N] (fp32 partials [splits * mpad][N] when splits > 1)
   int32_t mt, nt;          // tiles along M and N
-  int32_t bn;              // columns per tile, a multiple of 16 in 128..256
+  int32_t bn;              // columns per tile, a multiple of 16 in 64..256
   int32_t nrows, ncols;    // M, N (what lies past them is not stored)
+  int32_t mrows;           // rows of a tile per CTA, at most 128: the MMA's other rows hold leftovers, not stored
   int32_t nkb, nseg;       // 64-wide K blocks per segment, segments
   int32_t a_mn, b_mn;      // 1: MN-major
   int32_t b_by_rank;
-  int32_t splits, mpad;    // K splits; rows between two splits' partials (a multiple of 256)
+  int32_t splits, mpad;    // K splits; rows between two splits' partials (mt * 2 * mrows)
   int32_t unit0;           // first unit of this problem in the launch
   int32_t out_kind;        // 0 bf16, 1 fp32, 2 fp32 added to what is there
   int32_t gcol;            // partials of u | g: column of g's part

@@ -19,8 +19,9 @@ struct Product {
   int nkb;       // 64-wide K blocks in all
   bool dual;     // u and g side by side
   bool b_mn;     // B has n contiguous
+  bool a_mn;     // A has m contiguous
   // the plan
-  int bn, mt, nt, splits;
+  int bn, mrows, mt, nt, splits;
   int64_t part_ld, part_bytes;  // fp32 partials: row stride in elements, bytes over all splits
 };
 
@@ -29,18 +30,24 @@ int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 void shape_product(Product& p, int bn, int splits) {
   p.bn = bn;
   p.mt = (int)((p.M + kFfnTileM - 1) / kFfnTileM);
+  // The rows are spread evenly over the tiles and their two CTAs: an SM's share of the operands' bytes is
+  // what bounds small batches (333 tokens of 2048 x 2048: tiles of 176 rows instead of 256 and 77). Where A has
+  // m contiguous its boxes are 64 wide.
+  p.mrows = p.a_mn ? kFfnTileM / 2 : (int)round_up((p.M + 2 * p.mt - 1) / (2 * p.mt), 8);
   const int cols = p.dual ? bn / 2 : bn;
   p.nt = (int)((p.N + cols - 1) / cols);
   p.splits = splits;
   // a stored chunk is 32 columns wide and may start at any multiple of 8 below N: g's part starts
   // past the end of u's last chunk
   p.part_ld = p.dual ? 2 * (round_up(p.N, 16) + 32) : p.N;
-  p.part_bytes = splits > 1 ? (int64_t)splits * p.mt * kFfnTileM * p.part_ld * 4 : 0;
+  p.part_bytes = splits > 1 ? (int64_t)splits * p.mt * 2 * p.mrows * p.part_ld * 4 : 0;
 }
 
 // Picks the tile width and the K splits of one launch's products by an estimate in SM clocks:
 //  - a 64-wide K block of a 256 x bn tile takes 2 * bn clocks of the pair's tensor cores (4096 MACs
-//    an SM and clock), but no less than one round of the ring's barriers (420);
+//    an SM and clock), but no less than an SM's share of A (mrows rows) and B takes (72 bytes a clock;
+//    40 where few SMs read weights with n contiguous, whose boxes are 64 short rows: 4 tiles of dh for 128 tokens
+//    took 430 clocks a block), nor than the issuing threads take (230, with two blocks to a stage);
 //  - a unit's fill and drain that nothing overlaps takes about 2500;
 //  - with more than one unit a pair, the last round is as long as a full one;
 //  - partial sums cost a second launch (about 6000) and their bytes, written and read once.
@@ -58,16 +65,19 @@ void plan(Product* p, int n) {
     b_mn = b_mn || p[i].b_mn;
     most = std::max(most, p[i].nkb);
   }
-  for (int bn = 128; bn <= 256; bn += b_mn ? 128 : 16) {
+  for (int bn = b_mn ? 128 : 64; bn <= 256; bn += b_mn ? 128 : 16) {
     for (int L = most; L >= 4 || L == most; L = L / 2) {
       double total = 0, longest = 0, parts = 0;
       int64_t units = 0;
       for (int i = 0; i < n; ++i) {
-        const int s = std::min(16, (p[i].nkb + L - 1) / L);
-        shape_product(p[i], bn, s);
-        const double kb = (double)((p[i].nkb + s - 1) / s) * std::max(2.0 * bn, 420.0) + 4.0 * bn;
-        const int64_t u = (int64_t)p[i].mt * p[i].nt * s;
-        units += u;
+        shape_product(p[i], bn, std::min(16, (p[i].nkb + L - 1) / L));
+        units += (int64_t)p[i].mt * p[i].nt * p[i].splits;
+      }
+      const double rate = b_mn && units < kPlanPairs / 4 ? 40 : 72;
+      for (int i = 0; i < n; ++i) {
+        const int64_t u = (int64_t)p[i].mt * p[i].nt * p[i].splits;
+        const double kb = (double)((p[i].nkb + p[i].splits - 1) / p[i].splits) *
+                              std::max({2.0 * bn, (128 * p[i].mrows + 64 * bn) / rate, 230.0}) + 4.0 * bn;
         total += kb * u;
         longest = std::max(longest, kb);
         parts += p[i].part_bytes;
@@ -112,8 +122,8 @@ ForwardPlan plan_forward(int64_t T, int64_t H, int64_t D) {
     f.bytes = l.at;
     return f;
   }
-  f.up = Product{T, D, blocks_of(H), true, false};
-  f.down = Product{T, H, blocks_of(D), false, false};
+  f.up = Product{T, D, blocks_of(H), true, false, false};
+  f.down = Product{T, H, blocks_of(D), false, false, false};
   plan(&f.up, 1);
   plan(&f.down, 1);
   Layout l;
@@ -132,12 +142,12 @@ struct BackwardPlan {
 // Planned as if every gradient is asked for: a call that leaves some out runs the others' plan.
 BackwardPlan plan_backward(int64_t T, int64_t H, int64_t D) {
   BackwardPlan b{};
-  b.dh = Product{T, D, blocks_of(H), false, true};
+  b.dh = Product{T, D, blocks_of(H), false, true, false};
   plan(&b.dh, 1);
-  b.rest[0] = Product{T, H, 2 * blocks_of(D), false, true};
-  b.rest[1] = Product{D, H, blocks_of(T), false, true};
+  b.rest[0] = Product{T, H, 2 * blocks_of(D), false, true, false};
+  b.rest[1] = Product{D, H, blocks_of(T), false, true, true};
   b.rest[2] = b.rest[1];
-  b.rest[3] = Product{H, D, blocks_of(T), false, true};
+  b.rest[3] = Product{H, D, blocks_of(T), false, true, true};
   plan(b.rest, 4);
   Layout l;
   b.du = l.take(T * D * 2);
@@ -162,13 +172,13 @@ int operand(moe_handle* h, CUtensorMap* m, const void* p, int64_t inner, int64_t
 }
 
 // A result (or u, g on their way in) by 32-column chunks: 16-bit (64 bytes a row) or 32-bit elements (128 bytes).
-int result(moe_handle* h, CUtensorMap* m, void* p, int64_t cols, int64_t rows, bool f32, int64_t ld) {
-  return encode_map(h, m, p, cols, rows, (uint64_t)ld * (f32 ? 4 : 2), 32, 128,
+int result(moe_handle* h, CUtensorMap* m, void* p, int64_t cols, int64_t rows, bool f32, int64_t ld, int box_rows) {
+  return encode_map(h, m, p, cols, rows, (uint64_t)ld * (f32 ? 4 : 2), 32, box_rows,
                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                     f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-void fill_problem(FfnProblem& f, const Product& p, int nseg, bool a_mn, int unit0) {
+void fill_problem(FfnProblem& f, const Product& p, int nseg, int unit0) {
   f.mt = p.mt;
   f.nt = p.nt;
   f.bn = p.bn;
@@ -176,11 +186,12 @@ void fill_problem(FfnProblem& f, const Product& p, int nseg, bool a_mn, int unit
   f.ncols = (int)p.N;
   f.nseg = nseg;
   f.nkb = p.nkb / nseg;
-  f.a_mn = a_mn;
+  f.a_mn = p.a_mn;
   f.b_mn = p.b_mn;
   f.b_by_rank = p.dual;
   f.splits = p.splits;
-  f.mpad = p.mt * kFfnTileM;
+  f.mrows = p.mrows;
+  f.mpad = p.mt * 2 * p.mrows;
   f.unit0 = unit0;
   f.gcol = (int)(p.part_ld / 2);
 }
@@ -191,17 +202,17 @@ int units_of(const Product& p) { return p.mt * p.nt * p.splits; }
 int set_result(moe_handle* h, FfnProblem& f, const Product& p, void* out, int kind, void* parts) {
   if (p.splits > 1) {
     f.out_kind = 1;
-    return result(h, &f.out, parts, p.part_ld, (int64_t)p.splits * f.mpad, true, p.part_ld);
+    return result(h, &f.out, parts, p.part_ld, (int64_t)p.splits * f.mpad, true, p.part_ld, p.mrows);
   }
   f.out_kind = kind;
-  return result(h, &f.out, out, p.N, p.M, kind != 0, p.N);
+  return result(h, &f.out, out, p.N, p.M, kind != 0, p.N, p.mrows);
 }
 
 FfnReduce reduce_of(const Product& p, const void* parts, void* out, int kind) {
   FfnReduce r{};
   r.parts = static_cast<const float*>(parts);
   r.ld = p.part_ld;
-  r.split_stride = (int64_t)p.mt * kFfnTileM * p.part_ld;
+  r.split_stride = (int64_t)p.mt * 2 * p.mrows * p.part_ld;
   r.splits = p.splits;
   r.rows = (int)p.M;
   r.cols = (int)p.N;
@@ -284,16 +295,16 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   P.timeout_ns = h->timeout_ns;
   P.nprob = 1;
   // u and g side by side, h from the epilogue
-  fill_problem(P.p[0], f.up, 1, false, 0);
+  fill_problem(P.p[0], f.up, 1, 0);
   P.units = units_of(f.up);
   P.save = u != nullptr;
-  if ((rc = operand(h, &P.p[0].a[0], x, H, T, 128))) return rc;
+  if ((rc = operand(h, &P.p[0].a[0], x, H, T, f.up.mrows))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->up, H, D, f.up.bn / 2))) return rc;
   if ((rc = operand(h, &P.p[0].b[1], w->gate, H, D, f.up.bn / 2))) return rc;
   if ((rc = set_result(h, P.p[0], f.up, hb, 0, ws + f.up_parts))) return rc;
   if (u) {
-    if ((rc = result(h, &P.out2, u, D, T, false, D))) return rc;
-    if ((rc = result(h, &P.out3, g, D, T, false, D))) return rc;
+    if ((rc = result(h, &P.out2, u, D, T, false, D, f.up.mrows))) return rc;
+    if ((rc = result(h, &P.out3, g, D, T, false, D, f.up.mrows))) return rc;
   }
   if ((rc = cuda_rc(launch_ffn_gemm(P, kFfnSwiglu, h->ffn_pairs, st)))) return rc;
   if (f.up.splits > 1) {
@@ -304,9 +315,9 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   }
   // out = h W_down^T
   const int kind = out_bf16 ? 0 : 1;
-  fill_problem(P.p[0], f.down, 1, false, 0);
+  fill_problem(P.p[0], f.down, 1, 0);
   P.units = units_of(f.down);
-  if ((rc = operand(h, &P.p[0].a[0], hb, D, T, 128))) return rc;
+  if ((rc = operand(h, &P.p[0].a[0], hb, D, T, f.down.mrows))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->down, D, H, f.down.bn / 2))) return rc;
   if ((rc = set_result(h, P.p[0], f.down, out, kind, ws + f.down_parts))) return rc;
   if ((rc = cuda_rc(launch_ffn_gemm(P, kFfnStore, h->ffn_pairs, st)))) return rc;
@@ -356,15 +367,15 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   P.timeout_ns = h->timeout_ns;
   // dh = dout W_down, and du, dg and h from the epilogue
   P.nprob = 1;
-  fill_problem(P.p[0], b.dh, 1, false, 0);
+  fill_problem(P.p[0], b.dh, 1, 0);
   P.units = units_of(b.dh);
-  if ((rc = result(h, &P.in_u, const_cast<void*>(u), D, T, false, D))) return rc;
-  if ((rc = result(h, &P.in_g, const_cast<void*>(g), D, T, false, D))) return rc;
-  if ((rc = operand(h, &P.p[0].a[0], dout, H, T, 128))) return rc;
+  if ((rc = result(h, &P.in_u, const_cast<void*>(u), D, T, false, D, b.dh.mrows))) return rc;
+  if ((rc = result(h, &P.in_g, const_cast<void*>(g), D, T, false, D, b.dh.mrows))) return rc;
+  if ((rc = operand(h, &P.p[0].a[0], dout, H, T, b.dh.mrows))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->down, D, H, 64))) return rc;
   if ((rc = set_result(h, P.p[0], b.dh, du, 0, ws + b.dh_parts))) return rc;
-  if ((rc = result(h, &P.out2, dg, D, T, false, D))) return rc;
-  if ((rc = result(h, &P.out3, hb, D, T, false, D))) return rc;
+  if ((rc = result(h, &P.out2, dg, D, T, false, D, b.dh.mrows))) return rc;
+  if ((rc = result(h, &P.out3, hb, D, T, false, D, b.dh.mrows))) return rc;
   if ((rc = cuda_rc(launch_ffn_gemm(P, kFfnDSwiglu, h->ffn_pairs, st)))) return rc;
   if (b.dh.splits > 1) {
     FfnReduce r = reduce_of(b.dh, ws + b.dh_parts, du, 0);
@@ -389,10 +400,10 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   for (int i = 0; i < 4; ++i) {
     if (!want[i].out) continue;
     FfnProblem& f = P.p[n++];
-    fill_problem(f, b.rest[i], i == 0 ? 2 : 1, i != 0, units);
+    fill_problem(f, b.rest[i], i == 0 ? 2 : 1, units);
     units += units_of(b.rest[i]);
     for (int s = 0; s < (i == 0 ? 2 : 1); ++s) {
-      if ((rc = operand(h, &f.a[s], want[i].a[s], want[i].am, T, i == 0 ? 128 : 64))) return rc;
+      if ((rc = operand(h, &f.a[s], want[i].a[s], want[i].am, T, i == 0 ? b.rest[0].mrows : 64))) return rc;
       if ((rc = operand(h, &f.b[s], want[i].b[s], want[i].bn, i == 0 ? D : T, 64))) return rc;
     }
     if ((rc = set_result(h, f, b.rest[i], want[i].out, i == 0 ? 0 : wkind, ws + b.parts[i]))) return rc;

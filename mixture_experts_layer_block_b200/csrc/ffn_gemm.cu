@@ -2,7 +2,7 @@
 // (ffn.cuh gives the formulas) as one persistent GEMM on pairs of SMs.
 //
 // What bounds it: at training sizes the tensor cores; at a few hundred tokens the weights' bytes.
-// Each output tile of 256 x bn (bn <= 256) belongs to a cluster of two CTAs: one
+// Each output tile of up to 256 x bn (bn <= 256) belongs to a cluster of two CTAs: one
 // tcgen05.mma.cta_group::2 (M = 256) per 16-wide K step, issued by CTA 0, with 128 rows of A and
 // bn / 2 rows of B staged by each CTA. A pair moves 32 KB per SM and 64-wide K step where a
 // 128 x 256 tile on one SM needs 48 KB for the same work. Two accumulators fill the tensor memory,
@@ -43,8 +43,7 @@ namespace moe {
 namespace {
 
 constexpr int kFThreads = 256;
-constexpr int kFMaxStages = 8;
-constexpr int kFABytes = 128 * kBK * 2;  // 16 KB of A per CTA and stage
+constexpr int kFMaxStages = 20;
 constexpr int kFBoxBytes = 64 * 64 * 2;  // an MN-major box of 64 x 64
 constexpr int kFChunk = 32;              // columns per epilogue step
 constexpr int kFBarBytes = 512;
@@ -54,10 +53,14 @@ constexpr int kFSmem = 227 * 1024 - 1024;  // less the alignment slack
 __host__ __device__ constexpr int staging_bytes(int epi) {
   return (epi == kFfnStore ? 32 : (epi == kFfnSwiglu ? 48 : 56)) * 1024;
 }
-constexpr int kFInBytes = 16384;               // u and g of a chunk
+constexpr int kFInBytes = 16384;               // u and g of a chunk (of 128 rows)
 constexpr int kFOutOff = 2 * kFInBytes;        // du, dg and h of a chunk
 __host__ __device__ constexpr int ring_bytes(int epi) { return kFSmem - staging_bytes(epi) - kFBarBytes; }
 
+// A's bytes per CTA and stage: mrows rows of 128 bytes (a multiple of 8 rows, so that B begins on a 1024-byte
+// line), or two 64-wide boxes. The MMA reads 128 rows all the same: what lies past the box makes rows that are
+// not stored.
+__host__ __device__ inline int a_bytes(const FfnProblem& p) { return p.a_mn ? 2 * kFBoxBytes : p.mrows * kBK * 2; }
 // B's bytes per CTA and stage: bn / 2 rows of 128 bytes, or whole 64-wide boxes
 __host__ __device__ inline int b_bytes(int bn, int b_mn) {
   return b_mn ? ((bn / 2 + 63) / 64) * kFBoxBytes : (bn / 2) * 128;
@@ -96,6 +99,15 @@ __device__ __forceinline__ bool wait_bar_fast(uint64_t* bar, uint32_t parity, De
   return wait_bar(bar, parity, meta, s_abort, limit, site);
 }
 
+__host__ __device__ inline int most_block_bytes(const FfnParams& P) {
+  int most = 0;
+  for (int i = 0; i < P.nprob; ++i) {
+    const int b = a_bytes(P.p[i]) + b_bytes(P.p[i].bn, P.p[i].b_mn);
+    most = most > b ? most : b;
+  }
+  return (most + 1023) & ~1023;
+}
+
 struct Unit {
   int prob, m, n, split;
 };
@@ -132,7 +144,10 @@ __device__ __forceinline__ void split_range(const FfnProblem& p, int split, int&
 
 }  // namespace
 
-template <int kEpi>
+// kPer: 64-wide K blocks of a stage, 1 or 2. A stage's barriers, its commit and the loops around them take about 330
+// clocks of the threads that issue, where four MMAs of 128 columns take 256: with two blocks to a stage narrow
+// tiles are no longer bound by that (333 tokens of 2048 x 2048: 23.0 -> 21.4 us).
+template <int kEpi, int kPer>
 __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnParams P) {
   constexpr int kStagingTotal = staging_bytes(kEpi);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -159,10 +174,8 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   DeviceMeta* meta = P.meta;
   const int64_t limit = P.timeout_ns;
   const int64_t drain_limit = max(limit, (int64_t)2000000000);  // copies in flight are waited for whatever the limit
-  // one ring for the whole launch: its stage holds the largest product's operands
-  int stage_bytes = 0;
-  for (int i = 0; i < P.nprob; ++i) stage_bytes = max(stage_bytes, kFABytes + b_bytes(P.p[i].bn, P.p[i].b_mn));
-  stage_bytes = (stage_bytes + 1023) & ~1023;
+  // one ring for the whole launch: a block holds the largest product's operands of 64 k
+  const int block_bytes = most_block_bytes(P), stage_bytes = kPer * block_bytes;
   const int nst = min(kFMaxStages, (ring_bytes(kEpi) & ~1023) / stage_bytes);
 
   if (threadIdx.x == 0) {
@@ -216,40 +229,45 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      const uint32_t ring = smem_u32(smem) + (is_a ? 0 : kFABytes);
-      for (int id = pair; ok && id < P.units; id += npairs) {
+            for (int id = pair; ok && id < P.units; id += npairs) {
         const Unit t = find_unit_ffn(P, id);
         const FfnProblem& p = P.p[t.prob];
         int k0, k1;
         split_range(p, t.split, k0, k1);
         const int half = p.bn / 2;
         const bool mn = is_a ? p.a_mn : p.b_mn;
-        const int row = is_a ? t.m * kFfnTileM + (int)rank * 128
+        const int row = is_a ? t.m * 2 * p.mrows + (int)rank * p.mrows
                              : (p.b_by_rank ? t.n * half : t.n * p.bn + (int)rank * half);
         const bool two = mn && (is_a || half > 64);
-        const uint32_t bytes = is_a ? kFABytes : b_bytes(p.bn, p.b_mn);
+        const uint32_t ring = smem_u32(smem) + (is_a ? 0 : a_bytes(p));
+        const uint32_t bytes = is_a ? a_bytes(p) : b_bytes(p.bn, p.b_mn);
         const CUtensorMap* maps = is_a ? p.a : p.b;
         int seg = k0 >= p.nkb ? 1 : 0;
         int left = p.nkb * (seg + 1) - k0;
         int k = (k0 - seg * p.nkb) * kBK;
         const CUtensorMap* map = &maps[!is_a && p.b_by_rank ? (int)rank : seg];
         if (nfill == 0) griddep_wait();
-        for (int n = k1 - k0; n > 0; --n) {
+        for (int n = k1 - k0; n > 0; n -= kPer) {
           if (!wait_bar_fast(&empty[stage], phase ^ 1, meta, s_abort, limit, kSiteProducerEmpty)) { ok = false; break; }
-          const uint32_t dst = ring + stage * stage_bytes;
           const uint32_t fb = full_c0 + 8u * stage;
-          mbar_arrive_expect_tx_cluster(fb, bytes);
-          if (mn) {
-            tma_load_2d_pair(dst, map, fb, row, k);
-            if (two) tma_load_2d_pair(dst + kFBoxBytes, map, fb, row + 64, k);
-          } else {
-            tma_load_2d_pair(dst, map, fb, k, row);
-          }
-          k += kBK;
-          if (--left == 0) {  // the second segment's operands
-            k = 0;
-            map = &maps[!is_a && p.b_by_rank ? (int)rank : 1];
-          }
+          auto block = [&](uint32_t dst) {
+            if (mn) {
+              tma_load_2d_pair(dst, map, fb, row, k);
+              if (two) tma_load_2d_pair(dst + kFBoxBytes, map, fb, row + 64, k);
+            } else {
+              tma_load_2d_pair(dst, map, fb, k, row);
+            }
+            k += kBK;
+            if (--left == 0) {  // the second segment's operands
+              k = 0;
+              map = &maps[!is_a && p.b_by_rank ? (int)rank : 1];
+            }
+          };
+          const uint32_t dst = ring + stage * stage_bytes;
+          const bool both = kPer == 2 && n > 1;
+          mbar_arrive_expect_tx_cluster(fb, both ? 2 * bytes : bytes);
+          block(dst);
+          if (both) block(dst + block_bytes);
           ++nfill;
           if (++stage == (uint32_t)nst) { stage = 0; phase ^= 1; }
         }
@@ -283,15 +301,20 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * kAccCols;
-        for (int kb = k0; kb < k1; ++kb) {
+        for (int kb = k0; kb < k1; kb += kPer) {
           if (!wait_bar_fast(&full[stage], phase, meta, s_abort, limit, kSiteMmaFull)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + kFABytes;
-          const uint64_t ad = p.a_mn ? sdesc_mnmajor_sw128(a) : sdesc_kmajor_sw128(a);
-          const uint64_t bd = p.b_mn ? sdesc_mnmajor_sw128(b) : sdesc_kmajor_sw128(b);
+          auto block = [&](uint32_t a, bool onto) {
+            const uint32_t b = a + a_bytes(p);
+            const uint64_t ad = p.a_mn ? sdesc_mnmajor_sw128(a) : sdesc_kmajor_sw128(a);
+            const uint64_t bd = p.b_mn ? sdesc_mnmajor_sw128(b) : sdesc_kmajor_sw128(b);
 #pragma unroll
-          for (int kk = 0; kk < kBK / kUK; ++kk)
-            umma_bf16_pair(d, ad + kk * astep, bd + kk * bstep, idesc, (kb != k0) || kk != 0);
+            for (int kk = 0; kk < kBK / kUK; ++kk)
+              umma_bf16_pair(d, ad + kk * astep, bd + kk * bstep, idesc, onto || kk != 0);
+          };
+          const uint32_t a = smem_u32(smem + stage * stage_bytes);
+          block(a, kb != k0);
+          if (kPer == 2 && kb + 1 < k1) block(a + block_bytes, true);
           mma_issued = true;
           umma_commit_pair_mc(&empty[stage], 3);
           if (++stage == (uint32_t)nst) { stage = 0; phase ^= 1; }
@@ -314,7 +337,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       auto place = [&](Cursor& c) {
         const Unit t = find_unit_ffn(P, c.id);
         c.col = t.n * p.bn;
-        c.row = t.m * kFfnTileM + (int)rank * 128;
+        c.row = t.m * 2 * p.mrows + (int)rank * p.mrows;
       };
       auto next = [&](Cursor& c) {
         if (++c.cc == nchunk) {
@@ -331,7 +354,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         const uint32_t b = loads & 1;
         const uint32_t dst = smem_u32(staging) + b * kFInBytes;
         const int col = in.col + chunk_col(in.cc, p.bn);
-        mbar_arrive_expect_tx(&ug_full[b], kFInBytes);
+        mbar_arrive_expect_tx(&ug_full[b], 2 * p.mrows * kFChunk * 2);
         tma_load_2d(dst, &P.in_u, &ug_full[b], col, in.row);
         tma_load_2d(dst + 8192, &P.in_g, &ug_full[b], col, in.row);
         ++loads;
@@ -363,7 +386,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     __syncwarp();
   } else {
     // ----------------------------------- epilogue -----------------------------------
-    // Each thread owns one row of the CTA's 128. A step takes 32 columns: bf16 results are staged
+    // Each thread owns one row of the MMA's 128 in this CTA, of which the first mrows are stored. A step takes 32 columns: bf16 results are staged
     // as 64-byte rows (64-byte swizzle), fp32 ones as 128-byte rows, and stored by TMA.
     const int q = warp & 3;
     const int row = q * 32 + lane;
@@ -393,7 +416,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     for (int id = pair; id < P.units; id += npairs, ++it) {
       const Unit t = find_unit_ffn(P, id);
       const FfnProblem& p = P.p[t.prob];
-      const int m0 = t.m * kFfnTileM + (int)rank * 128;
+      const int m0 = t.m * 2 * p.mrows + (int)rank * p.mrows;
       // one thread waits for the accumulator and tells the other 127, so that the warps always
       // leave the loop together
       if (leader) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
@@ -648,9 +671,21 @@ namespace {
 
 typedef void (*FfnKernel)(const FfnParams);
 
-FfnKernel ffn_kernel(int epilogue) {
-  return epilogue == kFfnStore ? ffn_gemm_kernel<kFfnStore>
-                               : (epilogue == kFfnSwiglu ? ffn_gemm_kernel<kFfnSwiglu> : ffn_gemm_kernel<kFfnDSwiglu>);
+template <int kPer>
+FfnKernel ffn_kernel_of(int epilogue) {
+  return epilogue == kFfnStore
+             ? ffn_gemm_kernel<kFfnStore, kPer>
+             : (epilogue == kFfnSwiglu ? ffn_gemm_kernel<kFfnSwiglu, kPer> : ffn_gemm_kernel<kFfnDSwiglu, kPer>);
+}
+
+FfnKernel ffn_kernel(int epilogue, int per) { return per == 2 ? ffn_kernel_of<2>(epilogue) : ffn_kernel_of<1>(epilogue); }
+
+// Blocks of a stage: two where four such stages fit (with fewer, 128 x 128 tiles of 2048 tokens were slower, 24.9
+// us for 22.5) and no tile is so wide that its MMAs take longer than their issue.
+int blocks_per_stage(const FfnParams& p, int epilogue) {
+  int widest = 0;
+  for (int i = 0; i < p.nprob; ++i) widest = std::max(widest, (int)p.p[i].bn);
+  return widest <= 160 && ring_bytes(epilogue) >= 4 * 2 * most_block_bytes(p) ? 2 : 1;
 }
 
 }  // namespace
@@ -670,15 +705,16 @@ cudaError_t launch_ffn_gemm(const FfnParams& p, int epilogue, int pairs, cudaStr
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ffn_kernel(epilogue), p);
+  return cudaLaunchKernelEx(&cfg, ffn_kernel(epilogue, blocks_per_stage(p, epilogue)), p);
 }
 
 // Sets the kernels' shared-memory limits and returns how many 2-CTA clusters fit on the device at
 // once (0 if none).
 cudaError_t configure_ffn_kernels(int* max_pairs) {
   *max_pairs = 0;
-  for (int e = 0; e < 3; ++e) {
-    const cudaError_t rc = cudaFuncSetAttribute(ffn_kernel(e), cudaFuncAttributeMaxDynamicSharedMemorySize, kFSmem + 1024);
+  for (int e = 0; e < 6; ++e) {
+    const cudaError_t rc =
+        cudaFuncSetAttribute(ffn_kernel(e / 2, 1 + e % 2), cudaFuncAttributeMaxDynamicSharedMemorySize, kFSmem + 1024);
     if (rc != cudaSuccess) return rc;
   }
   cudaLaunchConfig_t cfg{};
@@ -692,7 +728,7 @@ cudaError_t configure_ffn_kernels(int* max_pairs) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(max_pairs, (void*)ffn_kernel(kFfnStore), &cfg);
+  return cudaOccupancyMaxActiveClusters(max_pairs, (void*)ffn_kernel(kFfnStore, 1), &cfg);
 }
 
 }  // namespace moe
