@@ -171,11 +171,13 @@ int operand(moe_handle* h, CUtensorMap* m, const void* p, int64_t inner, int64_t
   return encode_map(h, m, p, inner, outer, (uint64_t)inner * 2, kBK, rows);
 }
 
-// A result (or u, g on their way in) by 32-column chunks: 16-bit (64 bytes a row) or 32-bit elements (128 bytes).
-int result(moe_handle* h, CUtensorMap* m, void* p, int64_t cols, int64_t rows, bool f32, int64_t ld, int box_rows) {
-  return encode_map(h, m, p, cols, rows, (uint64_t)ld * (f32 ? 4 : 2), 32, box_rows,
+// A result (or u, g on their way in) by chunks: 32 fp32 or, where `wide`, 64 bf16 columns (128 bytes a row), or 32 bf16
+// columns (64 bytes).
+int result(moe_handle* h, CUtensorMap* m, void* p, int64_t cols, int64_t rows, bool f32, int64_t ld, int box_rows,
+           bool wide = false) {
+  return encode_map(h, m, p, cols, rows, (uint64_t)ld * (f32 ? 4 : 2), wide && !f32 ? 64 : 32, box_rows,
                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                    f32 || wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 void fill_problem(FfnProblem& f, const Product& p, int nseg, int unit0) {
@@ -198,14 +200,14 @@ void fill_problem(FfnProblem& f, const Product& p, int nseg, int unit0) {
 
 int units_of(const Product& p) { return p.mt * p.nt * p.splits; }
 
-// Where a product's tiles go: its result, or the splits' partials.
-int set_result(moe_handle* h, FfnProblem& f, const Product& p, void* out, int kind, void* parts) {
+// Where a product's tiles go: its result (`wide`: the only one, by 128-byte rows), or the splits' partials.
+int set_result(moe_handle* h, FfnProblem& f, const Product& p, void* out, int kind, void* parts, bool wide) {
   if (p.splits > 1) {
     f.out_kind = 1;
     return result(h, &f.out, parts, p.part_ld, (int64_t)p.splits * f.mpad, true, p.part_ld, p.mrows);
   }
   f.out_kind = kind;
-  return result(h, &f.out, out, p.N, p.M, kind != 0, p.N, p.mrows);
+  return result(h, &f.out, out, p.N, p.M, kind != 0, p.N, p.mrows, wide);
 }
 
 FfnReduce reduce_of(const Product& p, const void* parts, void* out, int kind) {
@@ -301,7 +303,7 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   if ((rc = operand(h, &P.p[0].a[0], x, H, T, f.up.mrows))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->up, H, D, f.up.bn / 2))) return rc;
   if ((rc = operand(h, &P.p[0].b[1], w->gate, H, D, f.up.bn / 2))) return rc;
-  if ((rc = set_result(h, P.p[0], f.up, hb, 0, ws + f.up_parts))) return rc;
+  if ((rc = set_result(h, P.p[0], f.up, hb, 0, ws + f.up_parts, false))) return rc;
   if (u) {
     if ((rc = result(h, &P.out2, u, D, T, false, D, f.up.mrows))) return rc;
     if ((rc = result(h, &P.out3, g, D, T, false, D, f.up.mrows))) return rc;
@@ -319,7 +321,7 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   P.units = units_of(f.down);
   if ((rc = operand(h, &P.p[0].a[0], hb, D, T, f.down.mrows))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->down, D, H, f.down.bn / 2))) return rc;
-  if ((rc = set_result(h, P.p[0], f.down, out, kind, ws + f.down_parts))) return rc;
+  if ((rc = set_result(h, P.p[0], f.down, out, kind, ws + f.down_parts, true))) return rc;
   if ((rc = cuda_rc(launch_ffn_gemm(P, kFfnStore, h->ffn_pairs, st)))) return rc;
   if (f.down.splits > 1)
     return cuda_rc(launch_ffn_reduce(reduce_of(f.down, ws + f.down_parts, out, kind), kFfnStore, h->num_sms, st));
@@ -373,7 +375,7 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   if ((rc = result(h, &P.in_g, const_cast<void*>(g), D, T, false, D, b.dh.mrows))) return rc;
   if ((rc = operand(h, &P.p[0].a[0], dout, H, T, b.dh.mrows))) return rc;
   if ((rc = operand(h, &P.p[0].b[0], w->down, D, H, 64))) return rc;
-  if ((rc = set_result(h, P.p[0], b.dh, du, 0, ws + b.dh_parts))) return rc;
+  if ((rc = set_result(h, P.p[0], b.dh, du, 0, ws + b.dh_parts, false))) return rc;
   if ((rc = result(h, &P.out2, dg, D, T, false, D, b.dh.mrows))) return rc;
   if ((rc = result(h, &P.out3, hb, D, T, false, D, b.dh.mrows))) return rc;
   if ((rc = cuda_rc(launch_ffn_gemm(P, kFfnDSwiglu, h->ffn_pairs, st)))) return rc;
@@ -406,7 +408,7 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
       if ((rc = operand(h, &f.a[s], want[i].a[s], want[i].am, T, i == 0 ? b.rest[0].mrows : 64))) return rc;
       if ((rc = operand(h, &f.b[s], want[i].b[s], want[i].bn, i == 0 ? D : T, 64))) return rc;
     }
-    if ((rc = set_result(h, f, b.rest[i], want[i].out, i == 0 ? 0 : wkind, ws + b.parts[i]))) return rc;
+    if ((rc = set_result(h, f, b.rest[i], want[i].out, i == 0 ? 0 : wkind, ws + b.parts[i], true))) return rc;
   }
   P.nprob = n;
   P.units = units;

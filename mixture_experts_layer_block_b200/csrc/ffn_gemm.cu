@@ -132,9 +132,11 @@ __device__ __forceinline__ Unit find_unit_ffn(const FfnParams& P, int id) {
   return t;
 }
 
-// First column of a tile's chunk `cc`. A width that is no multiple of 32 ends in a chunk that
+// First column of a tile's chunk `cc`. A width that is no multiple of the chunk's ends in a chunk that
 // overlaps the one before it: those columns are stored twice, with the same values.
-__device__ __forceinline__ int chunk_col(int cc, int width) { return min(cc * kFChunk, width - kFChunk); }
+__device__ __forceinline__ int chunk_col(int cc, int width, int chunk = kFChunk) {
+  return min(cc * chunk, width - chunk);
+}
 
 __device__ __forceinline__ void split_range(const FfnProblem& p, int split, int& k0, int& k1) {
   const int total = p.nkb * p.nseg;
@@ -386,8 +388,9 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     __syncwarp();
   } else {
     // ----------------------------------- epilogue -----------------------------------
-    // Each thread owns one row of the MMA's 128 in this CTA, of which the first mrows are stored. A step takes 32 columns: bf16 results are staged
-    // as 64-byte rows (64-byte swizzle), fp32 ones as 128-byte rows, and stored by TMA.
+    // Each thread owns one row of the MMA's 128 in this CTA, of which the first mrows are stored. A step
+    // takes 32 columns, or 64 of a single bf16 result: rows of 128 bytes (128-byte swizzle) or, of several bf16 results, 64
+    // (64-byte swizzle), stored by TMA.
     const int q = warp & 3;
     const int row = q * 32 + lane;
     const bool leader = (warp == 2 && lane == 0);
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
         *reinterpret_cast<uint4*>(buf + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     };
-    auto put_f32 = [&](uint8_t* buf, const uint32_t (&w)[32]) {
+    auto put_128 = [&](uint8_t* buf, const uint32_t (&w)[32]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         *reinterpret_cast<uint4*>(buf + row * 128 + ((j ^ (row & 7)) << 4)) =
@@ -436,17 +439,31 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       };
       if (kEpi == kFfnStore || p.splits > 1) {
         // partials of u | g: the tile's second half belongs to g's columns
-        const int width = p.b_by_rank ? p.bn / 2 : p.bn, per = (width + kFChunk - 1) / kFChunk;
+        const int width = p.b_by_rank ? p.bn / 2 : p.bn;
+        const int chunk = p.out_kind == 0 ? 2 * kFChunk : kFChunk, per = (width + chunk - 1) / chunk;
         const int nchunk = p.b_by_rank ? 2 * per : per;
 #pragma unroll 1
         for (int cc = 0; cc < nchunk; ++cc) {
           const int part = cc >= per ? 1 : 0;
-          const int c0 = chunk_col(cc - part * per, width);
+          const int c0 = chunk_col(cc - part * per, width, chunk);
           uint32_t v[32];
           tmem_ld_32x32b_x32(tacc + part * width + c0, v);
-          tmem_ld_wait();
-          if (cc == nchunk - 1) release();
           uint8_t* buf = staging + sb * 16384;
+          if (p.out_kind == 0) {
+            uint32_t x[32];
+            tmem_ld_32x32b_x32(tacc + c0 + kFChunk, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              v[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              x[j] = pack_bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[16 + j] = x[j];
+          } else {
+            tmem_ld_wait();
+          }
+          if (cc == nchunk - 1) release();
           if (leader) bulk_wait_group_read<1>();
           named_bar_sync(1, 128);
           if (p.out_kind == 2 && c0 < cc * kFChunk) {  // columns that the chunk before has added
@@ -454,14 +471,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
             for (int j = 0; j < kFChunk; ++j)
               if (c0 + j < cc * kFChunk) v[j] = 0;
           }
-          if (p.out_kind == 0) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            put_bf16(buf, pk);
-          } else {
-            put_f32(buf, v);
-          }
+          put_128(buf, v);
           fence_proxy_async_shared();
           named_bar_sync(1, 128);
           if (leader) {
