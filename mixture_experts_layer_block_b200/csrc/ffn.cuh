@@ -37,6 +37,7 @@ struct alignas(64) FfnProblem {
   int32_t unit0;           // first unit of this problem in the launch
   int32_t out_kind;        // 0 bf16, 1 fp32, 2 fp32 added to what is there
   int32_t gcol;            // partials of u | g: column of g's part
+  uint32_t panel_inv;      // 2^32 / (kFfnRaster * nt), rounded up
 };
 
 struct FfnParams {

@@ -196,6 +196,8 @@ void fill_problem(FfnProblem& f, const Product& p, int nseg, int unit0) {
   f.mpad = p.mt * 2 * p.mrows;
   f.unit0 = unit0;
   f.gcol = (int)(p.part_ld / 2);
+  const uint64_t panel = (uint64_t)kFfnRaster * p.nt;
+  f.panel_inv = (uint32_t)(((1ull << 32) + panel - 1) / panel);
 }
 
 int units_of(const Product& p) { return p.mt * p.nt * p.splits; }

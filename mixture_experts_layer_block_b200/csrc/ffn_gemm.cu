@@ -122,13 +122,26 @@ __device__ __forceinline__ Unit find_unit_ffn(const FfnParams& P, int id) {
     if (i < P.nprob && id >= P.p[i].unit0) t.prob = i;
   const FfnProblem& p = P.p[t.prob];
   id -= p.unit0;
-  t.split = id % p.splits;
-  const int tile = id / p.splits;
+  t.split = 0;
+  int tile = id;
+  if (p.splits > 1) {
+    t.split = id % p.splits;
+    tile = id / p.splits;
+  }
+  // tile / per by the reciprocal rounded up, which is one too many at most (four divisions took 500 clocks of every
+  // unit's epilogue, and of every role's start)
   const int per = kFfnRaster * p.nt;
-  const int first = tile / per * kFfnRaster, r = tile % per;
-  const int gm = min(kFfnRaster, p.mt - first);
-  t.m = first + r % gm;
-  t.n = r / gm;
+  int panel = (int)__umulhi((uint32_t)tile, p.panel_inv);
+  if (panel * per > tile) --panel;
+  const int first = panel * kFfnRaster, r = tile - panel * per;
+  if (p.mt - first >= kFfnRaster) {
+    t.m = first + r % kFfnRaster;
+    t.n = r / kFfnRaster;
+  } else {
+    const int gm = p.mt - first;
+    t.m = first + r % gm;
+    t.n = r / gm;
+  }
   return t;
 }
 
@@ -393,7 +406,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     // (64-byte swizzle), stored by TMA.
     const int q = warp & 3;
     const int row = q * 32 + lane;
-    const bool leader = (warp == 2 && lane == 0);
+    auto leader = [&]() { return warp == 2 && elect_one(); };  // always the same lane
     uint32_t acc = 0, acc_phase = 0, sb = 0, ug_phase = 0, out_phase = 0;
     auto get_bf16 = [&](const uint8_t* buf, uint32_t (&w)[16]) {
 #pragma unroll
@@ -422,10 +435,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       const int m0 = t.m * 2 * p.mrows + (int)rank * p.mrows;
       // one thread waits for the accumulator and tells the other 127, so that the warps always
       // leave the loop together
-      if (leader) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
+      if (leader()) s_go[it & 1] = wait_bar(&acc_full[acc], acc_phase, meta, s_abort, limit, kSiteEpiAcc) ? 1 : 0;
       named_bar_sync(1, 128);
       if (s_go[it & 1] == 0) {
-        if (leader) give_up();
+        if (leader()) give_up();
         break;
       }
       tc_fence_after();
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
             tmem_ld_wait();
           }
           if (cc == nchunk - 1) release();
-          if (leader) bulk_wait_group_read<1>();
+          if (leader()) bulk_wait_group_read<1>();
           named_bar_sync(1, 128);
           if (p.out_kind == 2 && c0 < cc * kFChunk) {  // columns that the chunk before has added
 #pragma unroll
@@ -474,7 +487,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           put_128(buf, v);
           fence_proxy_async_shared();
           named_bar_sync(1, 128);
-          if (leader) {
+          if (leader()) {
             const int c = t.n * width + c0, col = part * p.gcol + c;
             const bool in = rows_in && c < p.ncols;
             if (in) {
@@ -500,7 +513,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
             pk[j] = pack_bf16x2(swiglu(__uint_as_float(u[2 * j]), __uint_as_float(g[2 * j])),
                                 swiglu(__uint_as_float(u[2 * j + 1]), __uint_as_float(g[2 * j + 1])));
           uint8_t* buf = staging + sb * 24576;
-          if (leader) bulk_wait_group_read<1>();
+          if (leader()) bulk_wait_group_read<1>();
           named_bar_sync(1, 128);
           put_bf16(buf, pk);
           if (P.save) {
@@ -513,7 +526,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
           }
           fence_proxy_async_shared();
           named_bar_sync(1, 128);
-          if (leader) {
+          if (leader()) {
             const int col = t.n * hn + c0;
             if (rows_in && col < p.ncols) {
               tma_store_2d(&p.out, smem_u32(buf), col, m0);
@@ -565,7 +578,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
-    if (leader) bulk_wait_group<0>();
+    if (leader()) bulk_wait_group<0>();
   }
 
   griddep_launch_dependents();
