@@ -478,6 +478,9 @@ class MoELayer:
               "moe_ffn_forward")
         return out
 
+    _GRADS = frozenset(("x", "Ws_up", "Ws_gate", "Ws_down"))
+    _WEIGHT_GRADS = tuple((n, f"grads[{n!r}]") for n in ("Ws_up", "Ws_gate", "Ws_down"))
+
     def ffn_backward(self, dout, x, u, g, wts, grads, accumulate=False, workspace=None, stream=None):
         """moe_ffn_backward: fills grads["x"] ([T, H] bf16) and grads["Ws_up"], grads["Ws_gate"],
         grads["Ws_down"] (shaped as the weights, all bf16 or all fp32; with accumulate, fp32 and
@@ -487,16 +490,16 @@ class MoELayer:
         _is_tensor(dout, "dout", (T, H), _BF16, dev)
         _is_tensor(u, "u", (T, D), _BF16, dev)
         _is_tensor(g, "g", (T, D), _BF16, dev)
-        if not grads.keys() <= {"x", "Ws_up", "Ws_gate", "Ws_down"}:
+        if not grads.keys() <= self._GRADS:
             raise ValueError(f"gradients are named x, Ws_up, Ws_gate and Ws_down, got {sorted(grads)}")
         dx = grads.get("x")
         if dx is not None:
             _is_tensor(dx, "grads['x']", (T, H), _BF16, dev)
         first, addr = None, []
-        for n in ("Ws_up", "Ws_gate", "Ws_down"):
+        for n, name in self._WEIGHT_GRADS:
             t = grads.get(n)
             if t is not None:
-                _is_tensor(t, f"grads[{n!r}]", wts[n].shape, _F32 if accumulate else _BF16_F32, dev)
+                _is_tensor(t, name, wts[n].shape, _F32 if accumulate else _BF16_F32, dev)
                 first = t if first is None else first
                 if t.dtype != first.dtype:
                     raise TypeError("the weight gradients must all be bfloat16 or all float32")
