@@ -1,18 +1,19 @@
 // ffn_gemm.cu -- the matrix products of the gated feed-forward block and of its backward pass
 // (ffn.cuh gives the formulas) as one persistent GEMM on pairs of SMs.
 //
-// What bounds it: at training sizes the tensor cores; at a few hundred tokens the weights' bytes.
+// What bounds it: at training sizes the tensor cores; at a few hundred tokens the start and end of its
+// launches and the pace of the threads that issue TMA and MMA.
 // Each output tile of up to 256 x bn (bn <= 256) belongs to a cluster of two CTAs: one
-// tcgen05.mma.cta_group::2 (M = 256) per 16-wide K step, issued by CTA 0, with 128 rows of A and
-// bn / 2 rows of B staged by each CTA. A pair moves 32 KB per SM and 64-wide K step where a
+// tcgen05.mma.cta_group::2 (M = 256) per 16-wide K step, issued by CTA 0, with up to 128 rows of A
+// and bn / 2 rows of B staged by each CTA. A pair moves 32 KB per SM and 64-wide K step where a
 // 128 x 256 tile on one SM needs 48 KB for the same work. Two accumulators fill the tensor memory,
 // so that the epilogue of one tile runs under the products of the next.
 //
 // Operands come as they lie in memory. A K-major operand is one TMA box of {64 k, rows}; an
 // MN-major one (the weights of the backward products, and both operands of the weight gradients)
 // is boxes of {64 m or n, 64 k}, which the MMA reads through an MN-major descriptor: no transposed
-// copy is ever made. Everything past an edge is filled with zeros by TMA on both operands, and
-// clipped on the way out.
+// copy is ever made. Everything past an edge is filled with zeros by TMA on both operands (the MMA's rows past
+// a tile's own hold leftovers of the ring, each of which makes a row of its own), and clipped on the way out.
 //
 // The units (tile, K split) of up to four products form one list (the four gradients that depend
 // on du, dg and h run as one launch), dealt round robin to the pairs: with equal units per
@@ -31,8 +32,8 @@
 // Measured (one B200, T = 4096, H = 7168, D = 2048): u | g 177 us (1360 TFLOP/s), the four gradients 410 us
 // (1465 TFLOP/s), dh 100 us alone (1200 TFLOP/s; 128 tiles are 1.7 rounds of 74 pairs); cuBLAS does one of
 // these products at 1320-1480 TFLOP/s. Back to back, power holds both near 1300-1380. A pair's 32 KB per SM and
-// K block need 64 bytes a clock from L2 at full rate, which is all that an SM can take: tiles narrower
-// than 256 are bound by that.
+// K block need 64 bytes a clock from L2 at full rate, which is about all that an SM takes. 333 tokens of 2048 x
+// 2048: 20.8 us for both launches, 32 K blocks each at 250-330 clocks.
 #include <algorithm>
 
 #include "ffn.cuh"
