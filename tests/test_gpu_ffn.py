@@ -85,7 +85,9 @@ def _close(got, ref, err, name):
 SHAPES = [(1, 256, 128), (5, 264, 136), (16, 2048, 512), (17, 264, 136), (31, 8, 8), (64, 1024, 72), (127, 72, 1024),
           (128, 512, 256), (129, 2048, 512), (257, 328, 1032), (333, 2048, 200), (515, 2048, 512), (1030, 520, 1544),
           # few tokens and long sums over few tiles
-          (5, 264, 2048), (16, 2568, 2048), (9, 24, 4104), (2, 8, 8)]
+          (5, 264, 2048), (16, 2568, 2048), (9, 24, 4104), (2, 8, 8),
+          # rows spread over tiles that none of them fills; K split with the narrowest tiles; one K block
+          (777, 1024, 520), (20, 7168, 64), (40, 64, 2056), (200, 4104, 72), (513, 72, 72), (900, 264, 64)]
 
 
 @pytest.mark.parametrize("T,H,D", SHAPES)
