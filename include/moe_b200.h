@@ -386,10 +386,10 @@ MOE_API int moe_forward_host_join(moe_handle *h, void *stream, int32_t block);
 /* Synchronise the handle's last stream and report the device status word:
  * *device_status = 0 when every kernel since the last call finished normally, else a
  * device error code (bit 30 set, low bits naming the wait that ran out). The word is
- * cleared by this call. It also covers the moe_ffn_* calls: after one of their waits ran out, the
- * handle's later ones give up at once, until this call has reported it. Returns
- * MOE_ERR_DEVICE_TIMEOUT if a wait ran out, MOE_ERR_CUDA if the stream reported a CUDA error, else
- * MOE_OK. */
+ * cleared by this call, for the layer's calls and for the moe_ffn_* calls. After a wait ran out, later
+ * calls on the handle may give up early and leave their results unwritten; this call reports that and
+ * ends it. Returns MOE_ERR_DEVICE_TIMEOUT if a wait ran out, MOE_ERR_CUDA if the stream reported a CUDA
+ * error, else MOE_OK. */
 MOE_API int moe_get_status(moe_handle *h, int32_t *device_status);
 
 /* Stage entry points (each is one step of moe_forward, callable on its own).

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <cstddef>
 #include <new>
 #include <vector>
 
@@ -821,18 +822,19 @@ int moe_get_status(moe_handle* h, int32_t* device_status) {
     if (device_status) *device_status = 0;
     return MOE_ERR_CUDA;
   }
+  // The layer's words and the feed-forward block's own. An abort is cleared together with the status that it
+  // raised, never apart from it: a wait that gives up on an abort raises none of its own, and not every kernel
+  // sequence starts by clearing it (the 4-bit forward and the stage calls do not).
   int32_t st = 0;
-  if (cudaMemcpy(&st, &h->ws.meta->status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  const int32_t zero = 0;
-  if (cudaMemcpy(&h->ws.meta->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  // the feed-forward block's own words: an abort there stays until it is reported here
-  DeviceMeta fm{};
-  if (cudaMemcpy(&fm, h->ffn_meta, sizeof fm, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (fm.status != 0 || fm.abort != 0) {
-    if (cudaMemset(h->ffn_meta, 0, sizeof fm) != cudaSuccess) return MOE_ERR_CUDA;
-    if (st == 0) st = fm.status;
+  for (DeviceMeta* m : {h->ws.meta, h->ffn_meta}) {
+    DeviceMeta now{};
+    if (cudaMemcpy(&now, m, sizeof now, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
+    if (now.status == 0 && now.abort == 0) continue;
+    if (st == 0) st = now.status;
+    static_assert(offsetof(DeviceMeta, status) == offsetof(DeviceMeta, abort) + sizeof(int), "cleared in one piece");
+    // done before this returns: calls on streams that do not wait for the default one may follow
+    if (cudaMemset(&m->abort, 0, 2 * sizeof(int)) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   if (device_status) *device_status = st;
   if (st & kStatusTimeout) return MOE_ERR_DEVICE_TIMEOUT;

@@ -497,3 +497,38 @@ def test_overlapping_results_are_refused():
     layer.matvec_int4(x, square, ref)
     assert torch.equal(out, ref)
     layer.close()
+
+
+@pytest.mark.parametrize("first", [False, True])
+def test_forward_after_a_wait_that_ran_out(first):
+    """A wait of a bf16 forward runs out (stalled on the host's request). Once the status has said so, a
+    4-bit forward of the handle is the one that any other handle computes, whether its long router sum (4096 blocks of
+    64, which outlasts the first looks at its barriers) is the first that the handle computes or not."""
+    from mixture_experts_layer_block_b200.native import MOE_ERR_DEVICE_TIMEOUT
+    H, D, E, k, T = 1 << 18, 16, 4, 1, 16
+    g = torch.Generator(device="cuda").manual_seed(21)
+
+    def r(*shape, s=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * s).to(torch.bfloat16)
+
+    wts = {"W_router": r(E, H, s=H ** -0.5), "W_up": r(E, D, H, s=H ** -0.5), "W_gate": r(E, D, H, s=H ** -0.5),
+           "W_down": r(E, H, D, s=0.25)}
+    layer, other = (_layer(H, D, E, k, T=40, timeout_ns=limit) for limit in (50_000_000, 0))
+    packed = other.quantize_experts_int4(wts, 64)
+    x, before = r(T, H), r(40, H)
+    ref, out = (torch.empty(T, H, device="cuda") for _ in range(2))
+    other.forward_int4(x, wts["W_router"], None, packed, ref)
+    assert other.status() == (0, 0)
+    if not first:
+        layer.forward_int4(x.neg(), wts["W_router"], None, packed, out)
+    layer.inject_stall(1)
+    layer.forward(before, wts, torch.empty(40, H, device="cuda"))
+    rc, st = layer.status()
+    assert rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30)
+    for _ in range(2):
+        out.fill_(float("nan"))
+        layer.forward_int4(x, wts["W_router"], None, packed, out)
+        assert layer.status() == (0, 0)
+        assert torch.equal(out, ref)
+    layer.close()
+    other.close()
