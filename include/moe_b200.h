@@ -119,7 +119,8 @@ typedef struct moe_config {
     int32_t max_tokens;       /* largest T moe_forward will be called with, >= 1 */
     uint32_t flags;           /* MOE_FLAG_* */
     int32_t device;           /* CUDA device ordinal; -1 = the calling thread's current device */
-    int64_t timeout_ns;       /* limit of every device-side wait; <= 0 = 2e9 (2 s) */
+    int64_t timeout_ns;       /* limit of every device-side wait; <= 0 = 2e9 (2 s). After one ran out, what
+                               * is in flight is waited for longer: at least 2 s */
     int32_t claim_batch;      /* expert-GEMM tasks a CTA takes per claim on the shared counter,
                                * 0..64 (0 = 1). A CTA runs its batch's consecutive ids in order;
                                * larger batches mean fewer atomics on the counter but coarser load

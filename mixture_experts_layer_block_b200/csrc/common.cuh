@@ -250,9 +250,12 @@ static __device__ __noinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Dev
 }
 
 // Teardown wait: ignores the abort flag (the work it waits for is already in flight and will
-// finish), bounded by `limit_ns`.
+// finish), bounded by `limit_ns`, but never by less than two seconds: a CTA that left while a copy
+// or an MMA was still under way would have it land in the shared or tensor memory of the CTA after it.
+constexpr int64_t kMinDrainNs = 2000000000LL;
 static __device__ __noinline__ bool wait_bar_drain(uint64_t* bar, uint32_t parity, DeviceMeta* meta,
                                             int64_t limit_ns) {
+  if (limit_ns < kMinDrainNs) limit_ns = kMinDrainNs;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (static_cast<int64_t>(globaltimer_ns() - t0) > limit_ns) {

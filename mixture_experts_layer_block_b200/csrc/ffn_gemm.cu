@@ -189,7 +189,6 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   DeviceMeta* meta = P.meta;
   const int64_t limit = P.timeout_ns;
-  const int64_t drain_limit = max(limit, (int64_t)2000000000);  // copies in flight are waited for whatever the limit
   // one ring for the whole launch: a block holds the largest product's operands of 64 k
   const int block_bytes = most_block_bytes(P), stage_bytes = kPer * block_bytes;
   const int nst = min(kFMaxStages, (ring_bytes(kEpi) & ~1023) / stage_bytes);
@@ -397,7 +396,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       }
       bulk_wait_group<0>();
       for (uint32_t b = 0; b < 2; ++b)  // after an abort, loads that nobody waited for
-        if (loads > b) wait_bar_drain(&ug_full[b], ((loads - 1 - b) >> 1) & 1, meta, drain_limit);
+        if (loads > b) wait_bar_drain(&ug_full[b], ((loads - 1 - b) >> 1) & 1, meta, limit);
     }
     __syncwarp();
   } else {
@@ -599,11 +598,11 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
       for (int i = 0; i < 4; ++i) hi = max(hi, s_nfill[i]);
       for (int i = 0; i < 4; ++i)
         for (uint32_t j = s_nfill[i]; j < hi; ++j) mbar_arrive(&full[j % nst]);
-      drain_fills(full, nst, hi, meta, drain_limit);
+      drain_fills(full, nst, hi, meta, limit);
     }
     if (mma_issued) {  // in the thread that issued the MMAs
       umma_commit_pair(drain);
-      wait_bar_drain(drain, 0, meta, drain_limit);
+      wait_bar_drain(drain, 0, meta, limit);
     }
     __syncwarp();
     cluster_sync_all();

@@ -532,3 +532,19 @@ def test_forward_after_a_wait_that_ran_out(first):
         assert torch.equal(out, ref)
     layer.close()
     other.close()
+
+
+def test_forward_whose_own_wait_runs_out():
+    """A limit that the router's sum cannot keep: each 4-bit forward ends, and each is reported."""
+    from mixture_experts_layer_block_b200.native import MOE_ERR_DEVICE_TIMEOUT
+    H, D, E, k, T = 1 << 18, 16, 4, 1, 16
+    layer = _layer(H, D, E, k, timeout_ns=1_000)
+    _, packed = _experts(H, D, E, 0, 128, False, 90, layer)
+    x = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
+    wr = torch.ones(E, H, dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        layer.forward_int4(x, wr, None, packed, torch.empty(T, H, device="cuda"))
+        rc, st = layer.status()
+        assert rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30)
+        assert layer.status() == (0, 0)
+    layer.close()

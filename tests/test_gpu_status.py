@@ -96,3 +96,35 @@ def test_trace_records_and_wait_accounting(name, T, mx):
     assert np.all(col["mma_full"] + col["mma_acc"] + col["mma_task"] <= col["mma_loop"])
     assert np.all(col["prod_empty"] + col["prod_dep"] + col["prod_ring"] + col["prod_claim"] <= col["prod_loop"])
     assert np.all(col["epi_task"] + col["epi_acc"] <= col["epi_loop"])
+
+
+def _long_router(limit):
+    """A layer whose router sums 4096 blocks of 64 a CTA (about a millisecond), and its inputs."""
+    from mixture_experts_layer_block_b200.native import MoELayer
+    T, H, E = 16, 1 << 20, 2
+    layer = MoELayer(H, 16, E, 1, 16, T, timeout_ns=limit)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    wr = torch.randn(E, H, generator=g, device="cuda").to(torch.bfloat16)
+    return layer, x, wr
+
+
+def test_copies_in_flight_outlive_a_short_limit():
+    """A limit far below the time that a copy takes ends the router's waits with its ring full of copies:
+    they are waited for all the same, the status says what happened, and kernels behind it are right."""
+    from mixture_experts_layer_block_b200.native import MOE_ERR_DEVICE_TIMEOUT
+    hasty, x, wr = _long_router(1_000)
+    patient, _, _ = _long_router(0)
+    T, E = x.shape[0], wr.shape[0]
+    ref, got = (torch.empty(T, E, device="cuda") for _ in range(2))
+    patient.router_logits(x, wr, None, ref)
+    assert patient.status() == (0, 0)
+    for _ in range(5):
+        hasty.router_logits(x, wr, None, torch.empty(T, E, device="cuda"))
+        patient.router_logits(x, wr, None, got)
+        rc, st = hasty.status()
+        assert rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30)
+        assert patient.status() == (0, 0)
+        assert torch.equal(got, ref)
+    hasty.close()
+    patient.close()
