@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kRThreads, 1)
     const int q = warp & 3;
     const int row = q * 32 + lane;
     const int t = m0 + row;
-    const bool ok = wait_bar(acc_full, 0, meta, s_abort, timeout_ns, kSiteRouter);
+    // all lanes or none go on to the loads, which a warp issues as one: a limit may run out between two lanes' looks
+    const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, meta, s_abort, timeout_ns, kSiteRouter));
     tc_fence_after();
     if (ok) {
       for (int c = 0; c < BN; c += 16) {

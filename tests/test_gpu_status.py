@@ -128,3 +128,30 @@ def test_copies_in_flight_outlive_a_short_limit():
         assert torch.equal(got, ref)
     hasty.close()
     patient.close()
+
+
+def test_limits_about_as_long_as_the_sum():
+    """Limits from far below the router's time to far above it: each call either reports that a wait ran out
+    or is right."""
+    from mixture_experts_layer_block_b200.native import MOE_ERR_DEVICE_TIMEOUT, MoELayer
+    T, H, E = 128, 1 << 14, 64
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    wr = torch.randn(E, H, generator=g, device="cuda").to(torch.bfloat16)
+    ref = torch.empty(T, E, device="cuda")
+    patient = MoELayer(H, 16, E, 1, 16, T)
+    patient.router_logits(x, wr, None, ref)
+    assert patient.status() == (0, 0)
+    patient.close()
+    seen = set()
+    for limit in [1_000, 1_000_000] + [1_000 * us for us in range(10, 200, 5)]:
+        layer = MoELayer(H, 16, E, 1, 16, T, timeout_ns=limit)
+        for _ in range(4):
+            out = torch.full((T, E), float("nan"), device="cuda")
+            layer.router_logits(x, wr, None, out)
+            rc, st = layer.status()
+            assert (rc, st) == (0, 0) or (rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30))
+            assert rc != 0 or torch.equal(out, ref)
+            seen.add(rc)
+        layer.close()
+    assert seen == {0, MOE_ERR_DEVICE_TIMEOUT}
