@@ -400,7 +400,8 @@ MOE_API int moe_router_logits(moe_handle *h, const void *x, int32_t T, const voi
                       const float *router_bias, float *logits, void *stream);
 
 /* moe_gate_topk: per token, the top_k largest logits (ties to the lower expert index) in
- * descending order, and weights softmax(logits)[id] renormalised over the selected set.
+ * descending order, and weights softmax(logits)[id] renormalised over the selected set. NaN logits
+ * come last; the weights of a token that has to take one are NaN, as its output in a forward is.
  * logits device fp32 [T][E]; topk_ids device int32 [T][top_k]; topk_w device fp32
  * [T][top_k]. (Weave blog section 1.1; vLLM execution analysis, topk_softmax.) */
 MOE_API int moe_gate_topk(moe_handle *h, const float *logits, int32_t T, int32_t top_k,

@@ -20,6 +20,9 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The same, with NaN below everything (the key of -infinity is 0x007fffff).
+__device__ __forceinline__ uint32_t choice_key(float f) { return f != f ? 0u : order_key(f); }
+
 // Top-k with renormalised softmax for NT tokens at once (their dependency chains interleave):
 // v[n][j] holds expert lane + 32 j of token n. Each lane first sorts its VPL candidates of every
 // token (largest first, ties to the lower expert index; an odd-even merge network). Each of the
@@ -27,7 +30,8 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // the warp's largest head key (one redux), then the lowest expert index among the lanes whose
 // head holds it (another); the winning lane drops its head. Lane r < k returns round r's expert
 // in ids[n] and its weight exp(v_r - v_0) / sum_i exp(v_i - v_0) over the k chosen in w[n].
-// Experts >= E and NaN logits are never chosen while another candidate is left.
+// NaN logits come last, behind -infinity, by expert index; a token that has to take one has NaN weights. Experts
+// >= E are never chosen: k is at most E, so that every choice names an expert.
 template <int VPL>
 __device__ __forceinline__ void lane_sort_desc(uint32_t (&key)[VPL], int (&idx)[VPL], float (&val)[VPL]) {
   // compare-exchange (a, b): a keeps the larger key, the lower index on equal keys
@@ -66,7 +70,7 @@ __device__ __forceinline__ void warp_topk_scan_n(const float (&v)[NT][VPL], int 
     taken[n] = 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
-      if (lane + 32 * j >= E || v[n][j] != v[n][j]) taken[n] |= 1u << j;
+      if (lane + 32 * j >= E) taken[n] |= 1u << j;
   }
   for (int r = 0; r < k; ++r) {
     float bv[NT];
@@ -77,15 +81,16 @@ __device__ __forceinline__ void warp_topk_scan_n(const float (&v)[NT][VPL], int 
     for (int n = 0; n < NT; ++n) {
       bv[n] = -INFINITY;
       bi[n] = INT_MAX;
+      key[n] = 0u;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const int e = lane + 32 * j;
-        if (!((taken[n] >> j) & 1u) && (v[n][j] > bv[n] || (v[n][j] == bv[n] && e < bi[n]))) {
+      for (int j = 0; j < VPL; ++j) {  // rising indices: the first of equal keys is kept
+        const uint32_t kj = choice_key(v[n][j]);
+        if (!((taken[n] >> j) & 1u) && (bi[n] == INT_MAX || kj > key[n])) {
           bv[n] = v[n][j];
-          bi[n] = e;
+          bi[n] = lane + 32 * j;
+          key[n] = kj;
         }
       }
-      key[n] = bi[n] == INT_MAX ? 0u : order_key(bv[n]);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) best[n] = __reduce_max_sync(0xffffffffu, key[n]);
@@ -127,9 +132,8 @@ __device__ __forceinline__ void warp_topk_softmax_n(const float (&v)[NT][VPL], i
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       const int e = lane + 32 * j;
-      const bool ok = e < E && !(v[n][j] != v[n][j]);
-      key[n][j] = ok ? order_key(v[n][j]) : 0u;
-      idx[n][j] = ok ? e : INT_MAX;
+      key[n][j] = e < E ? choice_key(v[n][j]) : 0u;
+      idx[n][j] = e < E ? e : INT_MAX;
       val[n][j] = v[n][j];
     }
     lane_sort_desc<VPL>(key[n], idx[n], val[n]);
