@@ -384,7 +384,8 @@ MOE_API int moe_ffn_backward(moe_handle *h, const void *dout, const void *x, con
  * `block` non-zero the host also waits for them. */
 MOE_API int moe_forward_host_join(moe_handle *h, void *stream, int32_t block);
 
-/* Synchronise the handle's last stream and report the device status word:
+/* Synchronise the handle's last stream (the device, once the handle has been used for a moe_ffn_* call:
+ * those may be under way on several streams) and report the device status word:
  * *device_status = 0 when every kernel since the last call finished normally, else a
  * device error code (bit 30 set, low bits naming the wait that ran out). The word is
  * cleared by this call, for the layer's calls and for the moe_ffn_* calls. After a wait ran out, later

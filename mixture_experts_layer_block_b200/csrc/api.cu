@@ -818,7 +818,8 @@ int moe_get_status(moe_handle* h, int32_t* device_status) {
   if (!h) return MOE_ERR_INVALID_ARG;
   int rc;
   if ((rc = select_device(h))) return rc;
-  if (cudaStreamSynchronize(h->last_stream) != cudaSuccess) {
+  const bool all = h->ffn_used.load(std::memory_order_relaxed);
+  if ((all ? cudaDeviceSynchronize() : cudaStreamSynchronize(h->last_stream)) != cudaSuccess) {
     if (device_status) *device_status = 0;
     return MOE_ERR_CUDA;
   }

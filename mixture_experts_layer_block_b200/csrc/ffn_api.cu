@@ -267,7 +267,7 @@ int moe_ffn_forward(moe_handle* h, const void* x, int64_t T, int32_t hidden, int
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  h->last_stream = st;
+  h->ffn_used.store(true, std::memory_order_relaxed);
   char* ws = static_cast<char*>(workspace);
   void* hb = ws + f.h;
 
@@ -354,7 +354,7 @@ int moe_ffn_backward(moe_handle* h, const void* dout, const void* x, const void*
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  h->last_stream = st;
+  h->ffn_used.store(true, std::memory_order_relaxed);
   void* dw[3] = {gr.up, gr.gate, gr.down};
   const int wkind = (flags & MOE_FFN_GRAD_ADD) ? 2 : ((flags & MOE_FFN_GRAD_F32) ? 1 : 0);
   if (T == 0) {  // sums over no tokens

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <initializer_list>
 #include <vector>
@@ -89,6 +90,9 @@ struct moe_handle {
   // each layer forward resets, because such a call may run beside one on another stream
   moe::DeviceMeta* ffn_meta = nullptr;
   int ffn_pairs = 0;  // 2-CTA clusters of the block's GEMMs that fit on the device at once
+  // set by the first moe_ffn_* call that launches, from any thread: from then on moe_get_status waits for the device,
+  // since such calls may be under way on any number of streams, in replayed graphs too
+  std::atomic<bool> ffn_used{false};
 };
 
 namespace moe {

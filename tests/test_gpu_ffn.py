@@ -472,3 +472,62 @@ def test_a_wait_that_runs_out_is_reported(what):
     _close(out, ref, eo, "out")
     layer.close()
     patient.close()
+
+
+def _a_call_that_runs_out(layer):
+    """Arguments of a forward whose first tile sums 4096 blocks of 64 (a millisecond)."""
+    T, H, D = 37 * 256, 1 << 18, 256
+    assert layer.ffn_workspace_bytes(T, H, D) == 2 * T * D  # K is not split
+    wts = {"Ws_up": torch.zeros(D, H, dtype=torch.bfloat16, device="cuda"),
+           "Ws_gate": torch.zeros(D, H, dtype=torch.bfloat16, device="cuda"),
+           "Ws_down": torch.zeros(H, D, dtype=torch.bfloat16, device="cuda")}
+    return torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"), wts, torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+
+
+def test_the_status_covers_every_stream():
+    """A wait that runs out on one stream, behind tens of milliseconds of other work, is reported although the
+    handle's last call, on another stream, was over long before."""
+    from mixture_experts_layer_block_b200.native import MOE_ERR_DEVICE_TIMEOUT, MoELayer
+    layer = MoELayer(256, 128, 8, 2, 16, 16, timeout_ns=200_000)
+    long = _a_call_that_runs_out(layer)
+    x, wts, _ = _inputs(4, 264, 136, seed=1)
+    out = torch.empty_like(x)
+    busy = torch.zeros(1 << 32, dtype=torch.uint8, device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    layer.ffn_forward(x, wts, out, stream=b)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        for _ in range(20):  # 1.3 ms each at least
+            busy.add_(1)
+    layer.ffn_forward(*long, stream=a)
+    layer.ffn_forward(x, wts, out, stream=b)
+    rc, st = layer.status()
+    assert rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30)
+    assert layer.status() == (0, 0)
+    layer.close()
+
+
+def test_the_layers_counters_wait_for_the_layer():
+    """What the layer's last forward left is read behind that forward, not behind a later call of the block on
+    another stream."""
+    from mixture_experts_layer_block_b200 import configs, inputs as gen
+    from mixture_experts_layer_block_b200.native import MoELayer
+    w = configs.TINY
+    inp = {k: (v.cuda() if v is not None else None) for k, v in gen.make_inputs(w).items()}
+    layer = MoELayer.for_workload(w)
+    out = torch.empty((w.T, w.H), device="cuda")
+    layer.forward(inp["x"], inp, out)
+    tasks = layer.query(3)
+    x, wts, _ = _inputs(4, 264, 136, seed=1)
+    busy = torch.zeros(1 << 32, dtype=torch.uint8, device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    layer.forward(inp["x"][:1].contiguous(), inp, out[:1])
+    assert layer.query(3) < tasks
+    with torch.cuda.stream(a):
+        for _ in range(20):
+            busy.add_(1)
+    layer.forward(inp["x"], inp, out, stream=a)
+    layer.ffn_forward(x, wts, torch.empty_like(x), stream=b)
+    assert layer.query(3) == tasks
+    torch.cuda.synchronize()
+    layer.close()
