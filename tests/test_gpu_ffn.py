@@ -484,6 +484,36 @@ def _a_call_that_runs_out(layer):
     return torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"), wts, torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
 
 
+def test_a_handle_whose_wait_ran_out_works_again():
+    """Until the status is read, further calls return and the timeout stays to be reported; after it the same
+    handle's calls are right, forward and backward, and nothing is left to report."""
+    from mixture_experts_layer_block_b200.native import MOE_ERR_DEVICE_TIMEOUT, MoELayer
+    layer = MoELayer(256, 128, 8, 2, 16, 16, timeout_ns=200_000)
+    long = _a_call_that_runs_out(layer)
+    x, wts, dout = _inputs(200, 264, 136, seed=1)
+    out = torch.empty(200, 264, device="cuda")
+    u, g = (torch.empty(200, 136, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    grads = {"x": torch.empty_like(x), **{n: torch.empty_like(w) for n, w in wts.items()}}
+    for _ in range(2):
+        layer.ffn_forward(*long)
+        layer.ffn_forward(x, wts, out, u=u, g=g)
+        layer.ffn_backward(dout, x, u, g, wts, grads)
+        rc, st = layer.status()
+        assert rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30)
+        for t in (out, u, g, *grads.values()):
+            t.fill_(float("nan"))
+        layer.ffn_forward(x, wts, out, u=u, g=g)
+        ref, ru, rg, eo, eu, eg = _forward_reference(x, wts)
+        _close(out, ref, eo, "out")
+        _close(u, ru, eu, "u")
+        _close(g, rg, eg, "g")
+        layer.ffn_backward(dout, x, u, g, wts, grads)
+        for n, (r, e) in _backward_reference(dout, x, u, g, wts).items():
+            _close(grads[n], r, e, n)
+        assert layer.status() == (0, 0)
+    layer.close()
+
+
 def test_the_status_covers_every_stream():
     """A wait that runs out on one stream, behind tens of milliseconds of other work, is reported although the
     handle's last call, on another stream, was over long before."""
