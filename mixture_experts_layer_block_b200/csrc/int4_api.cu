@@ -48,6 +48,18 @@ int check_experts(const moe_handle* h, int32_t T, int32_t top_k, const moe_int4_
   return MOE_OK;
 }
 
+// Whether a call's result overlaps its experts' matrices: the down projection's CTAs store while others still
+// copy weights.
+bool overlaps_experts(const moe_config& c, const Span& out, const moe_int4_experts& w) {
+  auto in = [&](const moe_int4_mat& m, int64_t rows, int64_t cols) {
+    return overlap(out, {m.codes, int4_code_bytes(rows, cols)}) ||
+           overlap(out, {m.scales, int4_scale_bytes(rows, cols, w.group, w.zeros != 0)});
+  };
+  const int64_t E = c.num_experts, H = c.hidden, D = c.inter, Ds = c.inter_shared;
+  if (in(w.up, E * D, H) || in(w.gate, E * D, H) || in(w.down, E * H, D)) return true;
+  return Ds > 0 && (in(w.shared_up, Ds, H) || in(w.shared_gate, Ds, H) || in(w.shared_down, H, Ds));
+}
+
 // Up projections with SwiGLU into the workspace's h, then the down projections' weighted sum.
 int run_experts(moe_handle* h, const void* x, int32_t T, const int32_t* ids, const float* topk_w, int32_t k,
                 const moe_int4_experts* w, int capacity, void* out, bool out_bf16, cudaStream_t st) {
@@ -170,7 +182,8 @@ int moe_experts_int4(moe_handle* h, const void* x, int32_t T, const int32_t* top
   if (T > 0 && (!x || !topk_ids || !topk_w || !out)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(out)) return MOE_ERR_MISALIGNED;
   const int64_t n = (int64_t)T * h->cfg.hidden, slots = (int64_t)T * top_k;
-  if (clobbers({{out, n * (out_bf16 ? 2 : 4)}}, {{x, n * 2}, {topk_ids, slots * 4}, {topk_w, slots * 4}}))
+  const Span result{out, n * (out_bf16 ? 2 : 4)};
+  if (clobbers({result}, {{x, n * 2}, {topk_ids, slots * 4}, {topk_w, slots * 4}}) || overlaps_experts(h->cfg, result, *w))
     return MOE_ERR_INVALID_ARG;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
@@ -189,7 +202,11 @@ int moe_forward_int4(moe_handle* h, const void* x, int32_t T, const void* w_rout
   if (!w_router || (T > 0 && (!x || !out))) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(out) || !aligned16(router_bias)) return MOE_ERR_MISALIGNED;
   const int64_t n = (int64_t)T * h->cfg.hidden;
-  if (clobbers({{out, n * ((h->cfg.flags & MOE_FLAG_OUT_BF16) ? 2 : 4)}}, {{x, n * 2}})) return MOE_ERR_INVALID_ARG;
+  const Span result{out, n * ((h->cfg.flags & MOE_FLAG_OUT_BF16) ? 2 : 4)};
+  const int64_t E = h->cfg.num_experts;
+  if (clobbers({result}, {{x, n * 2}, {w_router, E * h->cfg.hidden * 2}, {router_bias, E * 4}}) ||
+      overlaps_experts(h->cfg, result, *w))
+    return MOE_ERR_INVALID_ARG;
   DeviceScope dev(h->device);
   if ((rc = dev.rc())) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -548,3 +548,47 @@ def test_forward_whose_own_wait_runs_out():
         assert rc == MOE_ERR_DEVICE_TIMEOUT and st & (1 << 30)
         assert layer.status() == (0, 0)
     layer.close()
+
+
+@pytest.mark.parametrize("Ds", [0, 32])
+def test_results_inside_the_weights_are_refused(Ds):
+    """A result that lies inside any matrix of the experts, or begins or ends in the router's weights or the bias,
+    is refused before anything is written."""
+    from mixture_experts_layer_block_b200 import native
+    H, D, E, k, T = 64, 32, 4, 2, 2
+    layer = _layer(H, D, E, k, inter_shared=Ds)
+    _, packed = _experts(H, D, E, Ds, 64, True, 15, layer)
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    ids, w = torch.tensor([[0, 1]] * T, dtype=torch.int32, device="cuda"), torch.full((T, k), 0.5, device="cuda")
+    big = torch.randn(64 * E * H, generator=g).cuda()
+    router, bias = big[:E * H // 2].view(torch.bfloat16).view(E, H), big[E * H:E * H + E]
+    kept = {n: (m.codes.clone(), m.scales.clone()) for n, m in packed.items()}
+    before = big.clone()
+
+    def refused(call):
+        with pytest.raises(native.MoEError) as err:
+            call()
+        assert err.value.code == native.MOE_ERR_INVALID_ARG
+
+    for m in packed.values():
+        for buf in (m.codes, m.scales):
+            out = buf[:2 * T * H].view(torch.bfloat16).view(T, H)
+            refused(lambda: layer.experts_int4(x, ids, w, packed, out))
+            if buf.numel() >= 4 * T * H:
+                out = buf[-4 * T * H:].view(torch.float32).view(T, H)
+                refused(lambda: layer.experts_int4(x, ids, w, packed, out))
+                refused(lambda: layer.forward_int4(x, router, None, packed, out))
+    for at in (0, E * H // 2 - 16, E * H + E - 4, E * H - T * H + 4):  # in the router's weights, at their end, in the bias
+        out = big[at:at + T * H].view(T, H)
+        refused(lambda: layer.forward_int4(x, router, bias, packed, out))
+    torch.cuda.synchronize()
+    assert torch.equal(big, before)
+    for n, m in packed.items():
+        assert torch.equal(m.codes, kept[n][0]) and torch.equal(m.scales, kept[n][1])
+    # right behind the router's weights, and in front of the bias: nothing overlaps
+    out, ref = big[E * H // 2:E * H // 2 + T * H].view(T, H), torch.empty(T, H, device="cuda")
+    layer.forward_int4(x, router, bias, packed, ref)
+    layer.forward_int4(x, router, bias, packed, out)
+    assert torch.equal(out, ref)
+    layer.close()
