@@ -304,7 +304,7 @@ MOE_API int moe_pack_int4(moe_handle *h, const uint8_t *q, const void *s, const 
 
 /* out[t] = W x[t]: x device bf16 [T][cols], out device [T][rows], bf16 (out_bf16 = 1, rounded once)
  * or fp32 (on its own type's boundary: rows may be any number). Any handle works. Any T (0..2^24),
- * but every 16 tokens are a launch that reads the weights again. rows up to 2^31 - 1. No scratch
+ * but every 16 tokens are a launch that reads the weights again. rows up to 2^31 - 16. No scratch
  * memory: calls on different streams may overlap. */
 MOE_API int moe_matvec_int4(moe_handle *h, const void *x, int64_t T, const moe_int4_mat *w, int64_t rows,
                             int64_t cols, int32_t group, int32_t zeros, void *out, int32_t out_bf16,

@@ -148,7 +148,8 @@ int moe_matvec_int4(moe_handle* h, const void* x, int64_t T, const moe_int4_mat*
   if ((rc = check_format(rows, cols, group))) return rc;
   if (T < 0 || !w || !has(*w)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!x || !out)) return MOE_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || T > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  // the kernel rounds rows up to whole tiles in 32 bits
+  if (rows > INT32_MAX - (kMvRows - 1) || T > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned(*w) || (reinterpret_cast<uintptr_t>(out) & (out_bf16 ? 1u : 3u)) != 0)
     return MOE_ERR_MISALIGNED;
   if (clobbers({{out, T * rows * (out_bf16 ? 2 : 4)}},

@@ -129,6 +129,17 @@ def test_int4_refusals(native):
     assert L.moe_forward_int4(None, P, 1, P, None, e, 1, P, None) == bad
 
 
+def test_matvec_rows_that_do_not_round_up_within_31_bits(native):
+    """The kernel's count of 16-row tiles is an int: the last sizes below 2^31 are refused, the first that fits
+    is not (the handle is, here)."""
+    def matvec(rows):
+        return native.lib.moe_matvec_int4(None, P, 1, native.moe_int4_mat(P << 20, P << 21), rows, 8, 32, 0, P << 30, 0, None)
+
+    for rows in ((1 << 31) - 15, (1 << 31) - 1, 1 << 31):
+        assert matvec(rows) == native.MOE_ERR_UNSUPPORTED, rows
+    assert matvec((1 << 31) - 16) == native.MOE_ERR_INVALID_ARG
+
+
 # ---- the binding -------------------------------------------------------------------------------------
 def _layer(native, H=64, D=32, E=4, k=2, Ds=0):
     layer = native.MoELayer.__new__(native.MoELayer)  # no handle: every call below is refused before the C call
