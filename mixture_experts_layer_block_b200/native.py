@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the layer runs in the library's CUDA kernels. The
 functions keep the C names; ``MoELayer`` is a convenience owner of a handle that takes torch
-tensors (device memory and streams come from PyTorch). There is no fallback: if the library
+tensors (device memory and streams come from PyTorch). torch is imported by the first call that needs it,
+so that the C functions can be had without it. There is no fallback: if the library
 is missing this module raises on import.
 """
 from __future__ import annotations
@@ -11,8 +12,6 @@ import ctypes
 import functools
 import math
 import os
-
-import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # MOE_B200_LIBRARY may name another build of the same library (for A/B timing of builds)
@@ -178,8 +177,14 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-_BF16, _F32, _U8, _I32S = (torch.bfloat16,), (torch.float32,), (torch.uint8,), (torch.int32,)
-_BF16_F32 = (torch.bfloat16, torch.float32)
+# the dtypes that a tensor may have; filled when the first tensor is looked at, which is when torch is there
+_BF16, _F32, _U8, _I32S, _BF16_F32 = [], [], [], [], []
+
+
+def _fill_dtypes():
+    import torch
+    _BF16[:], _F32[:], _U8[:], _I32S[:] = [torch.bfloat16], [torch.float32], [torch.uint8], [torch.int32]
+    _BF16_F32[:] = [torch.bfloat16, torch.float32]
 
 
 def _is_tensor(t, name, shape, dtypes, device):
@@ -190,6 +195,10 @@ def _is_tensor(t, name, shape, dtypes, device):
             return
     except AttributeError:
         pass
+    if not dtypes:
+        _fill_dtypes()
+        return _is_tensor(t, name, shape, dtypes, device)
+    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -205,9 +214,14 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-# the current stream's handle without making a Stream object (1 us less a call), where torch has it
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+def _current_raw_stream(device):
+    """The handle of the device's current stream. The first call puts torch's own function in this one's place,
+    which makes no Stream object (1 us less a call), where torch has it."""
+    global _current_raw_stream
+    import torch
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _current_raw_stream(device)
 
 
 def _raw_stream(stream, device):
@@ -225,6 +239,7 @@ class Int4Matrix:
         if nc < 0 or ns < 0:
             raise ValueError("4-bit matrices have columns in a multiple of 8 and groups of 32, 64 or 128 columns: "
                              f"got {rows}x{cols} with groups of {group}")
+        import torch
         self.codes = torch.empty(nc, dtype=torch.uint8, device=device)
         self.scales = torch.empty(ns, dtype=torch.uint8, device=device)
         self.rows, self.cols, self.group, self.zeros = rows, cols, group, 1 if zeros else 0
@@ -246,7 +261,6 @@ class MoELayer:
         check(lib.moe_init(ctypes.byref(self.cfg), ctypes.byref(h)), "moe_init")
         self.h = h
         self.device = self.query(13)
-        self._torch_device = torch.device("cuda", self.device)
         self.out_dtype = "bfloat16" if flags & MOE_FLAG_OUT_BF16 else "float32"
 
     def _check_out(self, out):
@@ -337,10 +351,12 @@ class MoELayer:
         return out
 
     def _int4_matrix(self, rows, cols, group, zeros, stream):
+        device = f"cuda:{self.device}"
         if stream is None:
-            return Int4Matrix(rows, cols, group, zeros, self._torch_device)
+            return Int4Matrix(rows, cols, group, zeros, device)
+        import torch
         with torch.cuda.stream(stream):
-            return Int4Matrix(rows, cols, group, zeros, self._torch_device)
+            return Int4Matrix(rows, cols, group, zeros, device)
 
     def quantize_experts_int4(self, wts, group=128, zeros=False, stream=None):
         """The experts of a weight dict (W_up, W_gate, W_down and, with a shared expert, Ws_up, Ws_gate,
@@ -447,6 +463,7 @@ class MoELayer:
         elif stream is None:
             workspace = x.new_empty(need >> 1)  # of x's 2-byte type: the cheapest allocation there is
         else:
+            import torch
             with torch.cuda.stream(stream):
                 workspace = x.new_empty(need >> 1)
         return workspace.data_ptr(), workspace.nbytes, workspace

@@ -113,3 +113,16 @@ def test_config_struct_matches_the_header(native):
     assert native.moe_config.timeout_ns.offset == 40
     assert native.moe_config.claim_batch.offset == 48
     assert ctypes.sizeof(native.moe_config) == 56
+
+
+def test_the_c_functions_need_no_torch(native):
+    """The binding loads and its C functions can be called where torch is not installed."""
+    import subprocess
+    import sys
+    code = ("import sys; sys.modules['torch'] = None\n"  # an import of it raises
+            "from mixture_experts_layer_block_b200 import native\n"
+            "assert native.lib.moe_int4_code_bytes(16, 128) == 1024\n"
+            "assert native.lib.moe_ffn_workspace_bytes(4, 64, 60, 0) == -1\n"
+            "assert native.lib.moe_init(None, None) == native.MOE_ERR_INVALID_ARG\n"
+            "assert native.MoELayer.ffn_workspace_bytes(4, 64, 32) >= 2 * 4 * 32")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
