@@ -3,6 +3,7 @@ dominant kernel's fraction of the HBM (or tensor) roofline.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl mine|reference]
                   [--workload dsv3] [--no-per-config] [--no-cpu-baseline] [--e2e-steps M]
+                  [--details FILE]
 
 One step = one whole layer forward (router projection, gating, align, row gather, expert
 GEMMs with the fused SwiGLU and router weighting, and the combine) over one batch of seeded
@@ -12,7 +13,8 @@ expert, 22.6 GB of expert weights, far larger than the 126 MB L2). The line also
 `per_config` object: every other workload (the FlashMoE-shaped prefill, decode on seeds 0, 1
 and 2, the skewed router and the same router without its bias, and the tiny layer), the
 static per-expert-quota ablation and the MXFP8 experts, each with its own timing, roofline
-fractions and SM-busy fraction, plus the skew overhead. Every timing is given twice: K
+fractions and SM-busy fraction, plus the skew overhead (the line holds the main figures of each, so
+that it stays a few KB; `--details FILE` writes everything that was measured). Every timing is given twice: K
 forwards back to back (the headline), and K forwards each after a write of a buffer twice the
 L2 size (outside the timed events).
 
@@ -667,6 +669,28 @@ def compact(entry):
     return d
 
 
+def brief(v):
+    """The main figures of a per_config entry as compact() gives it, with floats to 5 digits."""
+    def short(x):
+        return float(f"{x:.5g}") if isinstance(x, float) else x
+    d = {k: short(v[k]) for k in ("ms_per_step", "ms_per_step_l2_flushed", "tokens_per_s") if k in v}
+    d["gemm_frac"], d["layer_frac"] = short(v["gemm_roofline"].get("frac")), short(v["layer_roofline"]["frac"])
+    if v.get("scheduler", {}).get("sm_busy") is not None:
+        d["sm_busy"] = short(v["scheduler"]["sm_busy"])
+    d["sm_mhz"] = v["clocks"].get("sm_mhz")
+    slow = [r for r in v["clocks"].get("reasons") or [] if "slowdown" in r]
+    if slow:
+        d["reasons"] = slow
+    return d
+
+
+def printed(line):
+    """The line as it is printed: the other workloads' entries shortened."""
+    if "per_config" not in line:
+        return line
+    return {**line, "per_config": {k: brief(v) for k, v in line["per_config"].items()}}
+
+
 def run_profile(args, local):
     """--profile: the workload's warm-up and K timed forwards and nothing else (no flushed pass,
     no per-kernel timing pass, no host-buffer legs, no traced forward), for profiler captures."""
@@ -762,7 +786,10 @@ def run_mine(args, world, rank, local):
                             "uniform": u.get("scheduler", {}).get("sm_busy")},
                 "target": "<= 0.15 (time under skewed routing over uniform routing at equal useful FLOPs, minus 1)"}
     if rank == 0:
-        print(json.dumps(line))
+        if args.details:
+            with open(args.details, "w", encoding="utf-8") as fh:
+                json.dump(line, fh)
+        print(json.dumps(printed(line)))
     return 0
 
 
@@ -795,6 +822,7 @@ def main():
                     help="ncu dram bytes per launch of the expert-GEMM kernel, if captured")
     ap.add_argument("--profile", action="store_true",
                     help="only the warm-up and the K timed forwards of --workload (for profiler captures)")
+    ap.add_argument("--details", default=None, help="also write the line with every workload's full entry to this file")
     ap.add_argument("--claim-batch", type=int, default=0,
                     help="expert-GEMM task ids a CTA takes per claim on the shared counter (0 = 1)")
     args = ap.parse_args()

@@ -140,3 +140,26 @@ def test_kernel_source_hash_ignores_comments_only(tmp_path, monkeypatch):
     assert bench.kernel_source_hash() != base
     for w, rec in bench.MEASURED_TRAFFIC.items():
         assert bench.measured_traffic(w) is None
+
+
+def test_the_printed_line_stays_short():
+    """Every workload's main figures in a line of less than 8 KB; what is not shortened is unchanged."""
+    import json
+    v = 0.12345678901234567
+    entry = {"workload": "skew_uniform", "seed": 0, "precision": "bf16", "steps": 100, "ms_per_step": v,
+             "ms_per_step_l2_flushed": 12345.678901234567, "tokens_per_s": 741139.2710516216, "tflops": 590.2384773083501,
+             "stage_ms": {n: v for n in ("router", "gating", "align_scatter", "row_gather", "expert_gemm", "combine")},
+             "routing": {"kept_slots": 32768, "hit_experts": 256, "max_over_mean_load": v, "empty_experts_frac": v},
+             "gemm_shape": {"tile_m": 128, "workers": 148, "shape": 5, "scheduler": "dynamic", "kernels_per_forward": 6, "claim_batch": 1},
+             "scheduler": {"sm_busy": v, "makespan_us": v, "tasks": 11968, "waits": {str(i): v for i in range(25)}},
+             "clocks": {"sm_mhz": 1380.0, "sm_max_mhz": 1965.0, "reasons": ["sw_power_cap"], "samples": 16},
+             "gemm_roofline": {"bound": "tensor", "achieved": v, "unit": "TFLOP/s", "peak": v, "frac": v, "kernel_ms": v},
+             "layer_roofline": {"bound": "tensor", "frac": v, "frac_l2_flushed": v}}
+    keys = [k for k, *_ in bench.per_config_plan()] + ["dsv3"]
+    head = {"metric": bench.METRIC, "value": v, "e2e": {"value": v}, "rest": "x" * 3600}  # what the headline's own parts take
+    line = bench.printed({**head, "per_config": {k: entry for k in keys}})
+    assert len(json.dumps(line)) < 8000
+    assert {k: line[k] for k in head} == head and set(line["per_config"]) == set(keys)
+    got = line["per_config"]["skew"]
+    assert got["ms_per_step"] == 0.12346 and got["sm_busy"] == 0.12346 and got["gemm_frac"] == 0.12346
+    assert bench.printed(head) == head
