@@ -255,10 +255,10 @@ static __device__ __noinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Dev
 constexpr int64_t kMinDrainNs = 2000000000LL;
 static __device__ __noinline__ bool wait_bar_drain(uint64_t* bar, uint32_t parity, DeviceMeta* meta,
                                             int64_t limit_ns) {
-  if (limit_ns < kMinDrainNs) limit_ns = kMinDrainNs;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
-    if (static_cast<int64_t>(globaltimer_ns() - t0) > limit_ns) {
+    const int64_t dt = static_cast<int64_t>(globaltimer_ns() - t0);
+    if (dt > limit_ns && dt > kMinDrainNs) {
       atomicCAS(&meta->status, 0, kStatusTimeout | kSiteDrain);
       atomicExch(&meta->abort, 1);
       return false;

@@ -20,9 +20,6 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// The same, with NaN below everything (the key of -infinity is 0x007fffff).
-__device__ __forceinline__ uint32_t choice_key(float f) { return f != f ? 0u : order_key(f); }
-
 // Top-k with renormalised softmax for NT tokens at once (their dependency chains interleave):
 // v[n][j] holds expert lane + 32 j of token n. Each lane first sorts its VPL candidates of every
 // token (largest first, ties to the lower expert index; an odd-even merge network). Each of the
@@ -84,7 +81,7 @@ __device__ __forceinline__ void warp_topk_scan_n(const float (&v)[NT][VPL], int 
       key[n] = 0u;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {  // rising indices: the first of equal keys is kept
-        const uint32_t kj = choice_key(v[n][j]);
+        const uint32_t kj = v[n][j] != v[n][j] ? 0u : order_key(v[n][j]);  // NaN below -infinity's 0x007fffff
         if (!((taken[n] >> j) & 1u) && (bi[n] == INT_MAX || kj > key[n])) {
           bv[n] = v[n][j];
           bi[n] = lane + 32 * j;
@@ -132,8 +129,9 @@ __device__ __forceinline__ void warp_topk_softmax_n(const float (&v)[NT][VPL], i
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       const int e = lane + 32 * j;
-      key[n][j] = e < E ? choice_key(v[n][j]) : 0u;
-      idx[n][j] = e < E ? e : INT_MAX;
+      const bool ok = e < E && !(v[n][j] != v[n][j]);
+      key[n][j] = ok ? order_key(v[n][j]) : 0u;  // NaN and what is past E: lowest, by index, so past E last of all
+      idx[n][j] = e;
       val[n][j] = v[n][j];
     }
     lane_sort_desc<VPL>(key[n], idx[n], val[n]);
