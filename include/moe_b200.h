@@ -344,8 +344,9 @@ MOE_API int moe_forward_int4(moe_handle *h, const void *x, int32_t T, const void
  *   T       tokens, 0..2^24;  hidden H and inter D: multiples of 8, 8..2^20
  *   w       device bf16: up [D][H], gate [D][H], down [H][D]
  * MOE_ERR_INVALID_ARG for a null pointer, a bad size, a workspace that is too small, and for a result
- * or workspace that overlaps another buffer of the call (inputs may overlap one another), MOE_ERR_UNSUPPORTED for sizes beyond those above (and on a device
- * without room for a pair of SMs), MOE_ERR_MISALIGNED for a pointer off a 16-byte boundary. */
+ * or workspace that overlaps another buffer of the call (inputs may overlap one another);
+ * MOE_ERR_UNSUPPORTED for sizes beyond those above (and on a device without room for a pair of SMs);
+ * MOE_ERR_MISALIGNED for a pointer off a 16-byte boundary. */
 
 /* Workspace bytes of moe_ffn_forward (backward = 0) or moe_ffn_backward (1); -1 for sizes that
  * they refuse. */

@@ -47,7 +47,10 @@ void shape_product(Product& p, int bn, int splits) {
 //  - a 64-wide K block of a 256 x bn tile takes 2 * bn clocks of the pair's tensor cores (4096 MACs
 //    an SM and clock), but no less than an SM's share of A (mrows rows) and B takes (72 bytes a clock;
 //    40 where few SMs read weights with n contiguous, whose boxes are 64 short rows: 4 tiles of dh for 128 tokens
-//    took 430 clocks a block), nor than the issuing threads take (230, with two blocks to a stage);
+//    took 430 clocks a block), nor than the issuing threads take (230, with two blocks to a stage). The backward in us
+//    with 72 everywhere, 40 everywhere and the step at a quarter of the pairs: 128 tokens of 2048 x 512 19.1, 16.3,
+//    16.3; 257 tokens 19.3, 21.3, 17.9; 1000 tokens 30.1, 30.0, 26.8; 200 tokens of 4096 x 1536 44.0, 47.9, 44.0; but 300
+//    tokens of 7168 x 1024 54.8, 49.0, 54.8 and 128 tokens of 4096 x 4096 86.8, 78.3, 86.9;
 //  - a unit's fill and drain that nothing overlaps takes about 2500;
 //  - with more than one unit a pair, the last round is as long as a full one;
 //  - partial sums cost a second launch (about 6000) and their bytes, written and read once.

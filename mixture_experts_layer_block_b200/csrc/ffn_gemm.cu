@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_gemm_kernel(const __grid_con
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-            for (int id = pair; ok && id < P.units; id += npairs) {
+      for (int id = pair; ok && id < P.units; id += npairs) {
         const Unit t = find_unit_ffn(P, id);
         const FfnProblem& p = P.p[t.prob];
         int k0, k1;

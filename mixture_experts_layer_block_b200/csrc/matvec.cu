@@ -12,7 +12,8 @@
 //    unpacking as the A fragment, tokens are the N columns. tcgen05 would need the unpacked weights
 //    written back to shared memory, for products that take a fraction of the copy's time anyway;
 //  - 4-bit codes become bf16 exactly: (code | 0x4300) is 128 + code, less bf16(128 + zero). A group's
-//    sum is scaled in fp32, so nothing is rounded before the result;
+//    sum is scaled in fp32, so nothing of one product is rounded before its result. Of two, h is: to bf16, the
+//    operand type of the down product's MMA, as everywhere in the layer;
 //  - a kernel behind another of the same call may copy weights before that one is done.
 // The sums of a unit that several warps share meet in shared memory and are added in warp order: equal
 // inputs give equal bits.
