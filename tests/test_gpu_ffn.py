@@ -561,3 +561,74 @@ def test_the_layers_counters_wait_for_the_layer():
     assert layer.query(3) == tasks
     torch.cuda.synchronize()
     layer.close()
+
+
+def _product(a, b, ea=None):
+    """a b in fp64, and how far an fp32 sum of the rounded a may be off: additions of zeros are exact, so that only
+    the nonzero terms count."""
+    terms = (a != 0).double() @ (b != 0).double()
+    err = terms * R32 * (a.abs() @ b.abs())
+    return a @ b, err if ea is None else err + ea @ b.abs()
+
+
+@pytest.mark.parametrize("T,H,D", [(1, 1 << 20, 8), (16, 8, 1 << 20), (17, 1 << 20, 8), (40, 8, 1 << 20), (1 << 24, 8, 8),
+                                   (1 << 22, 16, 24)])
+def test_the_largest_extents(T, H, D):
+    """The longest rows, columns and batches that the block takes. What a long sum runs over is mostly zero, at random
+    places, so that its bound stays narrow."""
+    layer = _layer()
+    g = torch.Generator(device="cuda").manual_seed(H + D)
+
+    def r(*shape, keep=1.0, s=1.0):
+        v = torch.randn(shape, generator=g, device="cuda") * s
+        if keep < 1:
+            v *= torch.rand(shape, generator=g, device="cuda") < keep
+        return v.to(torch.bfloat16)
+
+    few = 1024.0
+    x, dout = (r(T, H, keep=few / H) if H > few else r(T, H) for _ in range(2))
+    if T > few:  # whole tokens
+        for v in (x, dout):
+            v *= (torch.rand(T, 1, generator=g, device="cuda") < few / T).to(torch.bfloat16)
+        x[-1], dout[-1] = 1.0, -1.0
+    wts = {"Ws_up": r(D, H, s=0.1 if H > few else 0.4), "Ws_gate": r(D, H, s=0.1 if H > few else 0.4),
+           "Ws_down": r(H, D, keep=few / D, s=0.1) if D > few else r(H, D, s=0.3)}
+    out = torch.empty(T, H, device="cuda")
+    u, gate = (torch.empty(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    layer.ffn_forward(x, wts, out, u=u, g=gate)
+    assert layer.status() == (0, 0)
+    up, gw, down = (wts[n].double() for n in ("Ws_up", "Ws_gate", "Ws_down"))
+    xd, dd = x.double(), dout.double()
+    ru, eu = _product(xd, up.T)
+    rg, eg = _product(xd, gw.T)
+    _close(u, ru, eu, "u")
+    _close(gate, rg, eg, "g")
+    s = torch.sigmoid(ru)
+    h = ru * s * rg
+    eh = 1.1 * rg.abs() * eu + (ru * s).abs() * eg + eu * eg + ACT * rg.abs() * (1 + ru.abs())
+    _close(out, *_product(h, down.T, eh + R16 * (h.abs() + eh)), "out")
+    del out, ru, rg, eu, eg, s, h, eh
+
+    grads = {"x": torch.empty_like(x), **{n: torch.empty_like(w, dtype=torch.float32) for n, w in wts.items()}}
+    layer.ffn_backward(dout, x, u, gate, wts, grads)
+    assert layer.status() == (0, 0)
+    ud, gd = u.double(), gate.double()
+    s = torch.sigmoid(ud)
+    a, da = ud * s, s * (1 + ud * (1 - s))
+    dh, e = _product(dd, down)
+    act = ACT * (1 + ud.abs())
+
+    def rounded(v, err):
+        return v, err + R16 * (v.abs() + err)
+
+    du, edu = rounded(dh * gd * da, e * (gd * da).abs() + (dh.abs() + e) * gd.abs() * act)
+    dg, edg = rounded(dh * a, e * a.abs() + (dh.abs() + e) * act)
+    h, eh = rounded(a * gd, gd.abs() * act)
+    del s, a, da, dh, e, act
+    # dx is one sum over both weights
+    _close(grads["x"], *_product(torch.cat((du, dg), 1), torch.cat((up, gw)), torch.cat((edu, edg), 1)), "x")
+    _close(grads["Ws_up"], *_product(du.T, xd, edu.T), "Ws_up")
+    _close(grads["Ws_gate"], *_product(dg.T, xd, edg.T), "Ws_gate")
+    ref, err = _product(dd.T, h)
+    _close(grads["Ws_down"], ref, err + dd.T.abs() @ eh, "Ws_down")
+    layer.close()

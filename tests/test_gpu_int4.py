@@ -592,3 +592,31 @@ def test_results_inside_the_weights_are_refused(Ds):
     layer.forward_int4(x, router, bias, packed, out)
     assert torch.equal(out, ref)
     layer.close()
+
+
+@pytest.mark.parametrize("R,K,group,zeros", [(5, 1 << 24, 128, False), (37, 1 << 22, 32, True), ((1 << 24) + 5, 8, 32, True),
+                                             (1 << 22, 40, 64, False)])
+def test_matvec_largest_extents(R, K, group, zeros):
+    """The longest rows and many rows. A long row's x is zero but at random places (additions of zeros are
+    exact, so that the bound counts the others)."""
+    layer = _layer()
+    g = torch.Generator(device="cuda").manual_seed(R + K)
+    G = -(-K // group)
+    q = torch.randint(0, 256, (R, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand(R, G, generator=g, device="cuda") + 0.1).to(torch.bfloat16)
+    z = torch.randint(0, 16, (R, G), generator=g, device="cuda", dtype=torch.uint8) if zeros else None
+    m = layer.pack_int4(q, s, z, group)
+    T = 3
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(K, device="cuda") if K < 2048 else torch.cat((torch.randint(0, K, (2000,), generator=g, device="cuda"),
+                                                                  torch.tensor([0, K - 1], device="cuda"))).unique()
+    x[:, at] = torch.randn(T, at.numel(), generator=g, device="cuda").to(torch.bfloat16)
+    code = torch.where(at % 2 == 0, q[:, at // 2] & 15, q[:, at // 2] >> 4).double()
+    w = (code - (8.0 if z is None else z[:, at // group].double())) * s[:, at // group].double()
+    xs = x[:, at].double()
+    ref, err = xs @ w.T, (2 * at.numel() + 8) * R32 * (xs.abs() @ w.abs().T)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full((T, R), float("nan"), dtype=dtype, device="cuda")
+        layer.matvec_int4(x, m, out)
+        _close(out, ref, err)
+    layer.close()
